@@ -328,6 +328,159 @@ nx_status nx_kv_compact(const nx_desc* desc, const void* k_cache, const void* v_
  */
 nx_status nx_read_device_status(const nx_desc* desc);
 
+/*
+ * ---- The decode step between two eviction events ----
+ *
+ * After an event every KV head holds its kept rows; until the next one, each new
+ * token is normed and rotated (nx_qk_norm_rope), appended (nx_paged_append) and
+ * attended over the cache (nx_paged_attn); nx_paged_gather reads the cached rows
+ * back in the layout of nx_evict_step / nx_evict_batch for the next event.
+ *
+ * The cache is paged and held in 8 bits.  Every (sequence, KV head) has its own
+ * page list and its own row count (per-head budgets leave heads of different
+ * lengths).  A page holds page_blocks blocks of NX_CACHE_BLOCK consecutive rows
+ * of one head; a block has one fp32 scale for K and one for V.  Rows past the
+ * last whole block (count % NX_CACHE_BLOCK of them) are held unquantised, in the
+ * call's element type, in a per-head tail, so a row is rounded to 8 bits once,
+ * together with its whole block.
+ *   k_codes [n_pages][page_blocks][32][D]     one byte per element
+ *   v_codes [n_pages][page_blocks][4][D][8]   row 8 g + j of the block at [g][d][j]
+ *   k_scale, v_scale [n_pages][page_blocks] fp32: an element is code * scale
+ *   k_tail [n_seqs][n_kv_heads][32][D], v_tail [n_seqs][n_kv_heads][4][D][8]
+ *   table [n_seqs][n_kv_heads][max_pages] int32 page numbers
+ *   lens  [n_seqs][n_kv_heads] int32 rows
+ * (V is stored 8 rows deep so that 8 consecutive bytes are one operand of the
+ * matrix instruction that sums over rows.)
+ *
+ * Conventions are those above, and: bases and strides of q, k, v, out and the
+ * cache arrays are multiples of 16 bytes (NX_EUNSUPPORTED otherwise).  A
+ * sequence whose row range, row count or page number is out of range is skipped
+ * (nx_paged_attn: its output rows are unspecified) and sets the bad-item bit of
+ * the device status.  A call's pages are distinct for the (sequence, head)s that
+ * it writes; pages that are only read may be shared.  The per-stage profiler
+ * covers the eviction stages only.  With NX_DEBUG set these calls are
+ * synchronous too.
+ */
+enum { NX_CACHE_E4M3 = 0, NX_CACHE_I8 = 1 };   /* 8-bit codes: OCP e4m3, signed integer */
+enum { NX_ROPE_HALF = 0, NX_ROPE_PAIRS = 1 };  /* pairs (i, i + rot/2), or (2i, 2i + 1) */
+#define NX_CACHE_BLOCK 32
+
+/* Rows of several heads: row r of head h starts at p + r * row_stride + h * head_stride
+ * elements and holds head_dim contiguous elements of the call's dtype. */
+typedef struct nx_rows {
+  void* p;
+  int64_t row_stride;
+  int64_t head_stride;
+} nx_rows;
+
+/* Position rotation: (a, b) -> (a cos - b sin, b cos + a sin) for the rot_dim / 2 pairs
+ * in the first rot_dim elements of a row; the others pass through. */
+typedef struct nx_rope {
+  const float* cos_sin;      /* [n_pos][rot_dim]: rot_dim / 2 cosines, then the sines; device */
+  const int32_t* positions;  /* nullable: table row of every row of the call; NULL: row r uses
+                                table row r.  A row outside [0, n_pos) marks the call bad in the
+                                device status and uses table row 0 */
+  int32_t n_pos;
+  int32_t rot_dim;           /* a multiple of 16, at most head_dim */
+  int32_t style;             /* NX_ROPE_HALF or NX_ROPE_PAIRS */
+} nx_rope;
+
+typedef struct nx_paged {
+  int32_t n_seqs;
+  int32_t n_q_heads;         /* a multiple of n_kv_heads, at most 256 per KV head */
+  int32_t n_kv_heads;
+  int32_t head_dim;          /* 64 or 128 */
+  int32_t dtype;             /* NX_BF16 or NX_F32: q, k, v, the tails and the outputs */
+  int32_t format;            /* NX_CACHE_E4M3 or NX_CACHE_I8 */
+  int32_t page_blocks;       /* blocks per page: a power of two, at most 1024 */
+  int32_t n_pages;
+  int32_t max_pages;         /* table entries per (sequence, head) */
+  void* k_codes;
+  void* v_codes;
+  float* k_scale;
+  float* v_scale;
+  void* k_tail;
+  void* v_tail;
+  const int32_t* table;
+  int32_t* lens;
+  void* workspace;           /* >= nx_paged_workspace_bytes(), zero-filled once before first use */
+  size_t workspace_bytes;
+  void* stream;
+} nx_paged;
+
+/*
+ * Workspace bytes of the nx_paged_* calls with up to max_tokens cached rows per
+ * head and max_q queries per sequence (append and gather need only the status
+ * word: any workspace of >= 256 bytes).  0 if the description is invalid.
+ */
+size_t nx_paged_workspace_bytes(const nx_paged* cache, int32_t max_tokens, int32_t max_q);
+
+/*
+ * Root-mean-square norm of every query and key head, then the position rotation,
+ * in one pass: y = x * weight / sqrt(mean(x^2) + eps), rounded once after the
+ * rotation.  Statistics and rotation are fp32.
+ *   desc      n_q_heads, n_kv_heads, head_dim, dtype, stream, and a workspace of
+ *             >= 256 bytes for the status word
+ *   rope      nullable: no rotation
+ *   q, out_q  n_rows rows of n_q_heads heads; out_q may be q itself (same base and strides)
+ *   k, out_k  nullable pair: n_rows rows of n_kv_heads heads
+ *   q_weight, k_weight   [head_dim] of the call's dtype; NULL: that side is not normed
+ */
+nx_status nx_qk_norm_rope(const nx_desc* desc, const nx_rope* rope, int32_t n_rows,
+                          const nx_rows* q, const nx_rows* out_q, const void* q_weight,
+                          const nx_rows* k, const nx_rows* out_k, const void* k_weight, float eps);
+
+/*
+ * Appends new K / V rows to every (sequence, head), K rotated on the way.
+ *   k, v       n_rows rows of n_kv_heads heads
+ *   new_start  nullable [n_seqs + 1] int32 (device): sequence s appends rows new_start[s] ..
+ *              new_start[s + 1] - 1, at most max_new; NULL: rows s * max_new ..
+ *              (s + 1) * max_new - 1
+ *   head_new   nullable [n_seqs][n_kv_heads] int32 (device): (s, h) appends only the first
+ *              head_new[s][h] of its sequence's rows (0 .. the sequence's row count)
+ *   lens_out   nullable [n_seqs][n_kv_heads]: the row counts after the call; NULL: cache->lens
+ *              itself is advanced
+ * A row is rotated in fp64 and rounded to the call's dtype; when its block is full
+ * the block's scale is s = amax * (1 / M) (M = 448 or 127; a block whose largest
+ * magnitude is at most 2^-100 has s = 0 and codes 0) and its codes are
+ * x * ((1 / amax) * M) rounded to nearest even, each operation rounded to fp32.  A non-finite element is stored as 0 and
+ * recorded in the device status (NX_ENONFINITE).  A sequence whose rows do not fit
+ * its table is left as it was and marked bad.
+ */
+nx_status nx_paged_append(const nx_paged* cache, const nx_rope* rope, const nx_rows* k,
+                          const nx_rows* v, int32_t n_rows, const int32_t* new_start,
+                          const int32_t* head_new, int32_t max_new, int32_t* lens_out);
+
+/*
+ * Attention of each sequence's queries over its cached rows.  Query i of a
+ * sequence with m queries sees the rows t <= n - m + i of a head of n rows (the
+ * queries' own rows are the last m; all are seen at m = 1).  A query that sees no
+ * row gives a zero output and lse = -infinity.  Query head g reads KV head
+ * g / (n_q_heads / n_kv_heads).
+ *   q, out     n_rows rows of n_q_heads heads (they must not overlap)
+ *   q_start    nullable [n_seqs + 1] int32 (device): sequence s has the rows q_start[s] ..
+ *              q_start[s + 1] - 1, at most max_q; NULL: max_q rows each.  Rows of no sequence
+ *              are left as they were
+ *   max_tokens expected largest row count (sizes the grid only: any value is correct, a close
+ *              bound is fastest); max_q: bound on the queries of a sequence
+ *   scale      factor of q . k; 0: 1 / sqrt(head_dim)
+ *   out_lse    nullable [n_rows][n_q_heads] fp32: ln of the sum of exp(scale q . k)
+ * The result does not depend on the order in which workgroups run.
+ */
+nx_status nx_paged_attn(const nx_paged* cache, const nx_rows* q, const nx_rows* out, int32_t n_rows,
+                        const int32_t* q_start, int32_t max_tokens, int32_t max_q, float scale,
+                        float* out_lse);
+
+/*
+ * The cached rows as contiguous rows of the call's dtype: row t < lens[s][h] of
+ * (s, h) at out_k + s * out_seq_stride + h * out_head_stride + t * head_dim
+ * elements, and likewise for V; other rows are left as they were.  max_tokens
+ * bounds the counts (a longer head is marked bad and skipped);
+ * out_head_stride >= max_tokens * head_dim.
+ */
+nx_status nx_paged_gather(const nx_paged* cache, int32_t max_tokens, void* out_k, void* out_v,
+                          int64_t out_seq_stride, int64_t out_head_stride);
+
 /* Human-readable name of a status code.  Pure host function. */
 const char* nx_status_str(nx_status status);
 

@@ -17,6 +17,8 @@ Modules
              as easy as 1, 2, 3", SC'11), in numpy uint64 arithmetic.
   nexus      the eviction step: window attention, Nexus walk, weights,
              A-Res keys, selection, compaction.
+  paged      the decode step between events: norm, rotation, 8-bit paged cache,
+             attention over it.
   enumerate  exact inclusion probabilities of weighted sampling without
              replacement by enumeration of orders (N <= 8).
 
@@ -24,4 +26,4 @@ Pinning status (what each function is checked against) is listed in the
 header of each module.
 """
 
-from . import philox, nexus, enumerate  # noqa: F401
+from . import philox, nexus, enumerate, paged  # noqa: F401

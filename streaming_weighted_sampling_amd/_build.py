@@ -13,7 +13,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_objs")
 LIB = os.path.join(HERE, "libnexus.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-SOURCES = ["score.hip", "reservoir.hip", "compact.hip", "abi.cpp"]
+SOURCES = ["score.hip", "reservoir.hip", "compact.hip", "abi.cpp", "paged.hip", "paged_attn.hip",
+           "paged_abi.cpp"]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17", "-Wall",
     # Packed fp32 VALU ops stay disabled (plain v_fma_f32 / v_add_f32 only).

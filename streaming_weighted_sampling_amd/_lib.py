@@ -22,6 +22,11 @@ NX_MAX_ALLOC_HEADS = 256
 NX_SCRATCH_BYTES = 16 << 20
 NX_BF16 = 0
 NX_F32 = 1
+NX_CACHE_E4M3 = 0
+NX_CACHE_I8 = 1
+NX_CACHE_BLOCK = 32
+NX_ROPE_HALF = 0
+NX_ROPE_PAIRS = 1
 
 
 class NxDesc(ctypes.Structure):
@@ -78,6 +83,49 @@ class NxUnit(ctypes.Structure):
     ]
 
 
+class NxRows(ctypes.Structure):
+    _fields_ = [
+        ("p", ctypes.c_void_p),
+        ("row_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+    ]
+
+
+class NxRope(ctypes.Structure):
+    _fields_ = [
+        ("cos_sin", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("n_pos", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("style", ctypes.c_int32),
+    ]
+
+
+class NxPaged(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32),
+        ("n_q_heads", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("format", ctypes.c_int32),
+        ("page_blocks", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("k_codes", ctypes.c_void_p),
+        ("v_codes", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("k_tail", ctypes.c_void_p),
+        ("v_tail", ctypes.c_void_p),
+        ("table", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.POINTER
 _VP = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -94,6 +142,14 @@ SIGNATURES = {
     "nx_kv_compact": (_I32, [_P(NxDesc), _VP, _VP, _VP, _I32, _I32, _VP, _VP]),
     "nx_head_budgets": (_I32, [_P(NxDesc), _VP, _I32, _I32, _I32, _VP]),
     "nx_read_device_status": (_I32, [_P(NxDesc)]),
+    "nx_paged_workspace_bytes": (ctypes.c_size_t, [_P(NxPaged), _I32, _I32]),
+    "nx_qk_norm_rope": (_I32, [_P(NxDesc), _P(NxRope), _I32, _P(NxRows), _P(NxRows), _VP,
+                               _P(NxRows), _P(NxRows), _VP, ctypes.c_float]),
+    "nx_paged_append": (_I32, [_P(NxPaged), _P(NxRope), _P(NxRows), _P(NxRows), _I32, _VP, _VP,
+                               _I32, _VP]),
+    "nx_paged_attn": (_I32, [_P(NxPaged), _P(NxRows), _P(NxRows), _I32, _VP, _I32, _I32,
+                             ctypes.c_float, _VP]),
+    "nx_paged_gather": (_I32, [_P(NxPaged), _I32, _VP, _VP, ctypes.c_int64, ctypes.c_int64]),
     "nx_stream_read": (_I32, [_VP, ctypes.c_size_t, _I32, _I32, _VP, _VP]),
     "nx_status_str": (ctypes.c_char_p, [_I32]),
     "nx_profile_enable": (_I32, [_I32]),

@@ -200,11 +200,10 @@ bool debug_mode() {
   return e != nullptr && e[0] != '\0' && !(e[0] == '0' && e[1] == '\0');
 }
 
-nx_status debug_check(const Args& a, hipStream_t s, int stage) {
+nx_status debug_check(const uint32_t* status, hipStream_t s, const char* name) {
   hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
   if (hipStreamIsCapturing(s, &cap) != hipSuccess) return NX_EHIP;
   if (cap != hipStreamCaptureStatusNone) return NX_OK;
-  const char* name = nx_stage_name(stage);
   hipError_t err = hipStreamSynchronize(s);
   if (err == hipSuccess) err = hipGetLastError();
   if (err != hipSuccess) {
@@ -212,8 +211,8 @@ nx_status debug_check(const Args& a, hipStream_t s, int stage) {
     return NX_EHIP;
   }
   uint32_t word = 0;
-  if (a.status != nullptr &&
-      hipMemcpy(&word, a.status, sizeof(word), hipMemcpyDeviceToHost) != hipSuccess)
+  if (status != nullptr &&
+      hipMemcpy(&word, status, sizeof(word), hipMemcpyDeviceToHost) != hipSuccess)
     return NX_EHIP;
   const nx_status st = (word & kStatusNonFinite) ? NX_ENONFINITE
                        : (word & kStatusBadItem) ? NX_EINVAL
@@ -302,7 +301,7 @@ nx_status enqueue(const Args& a, hipStream_t s, int first, int last, bool profil
       default: break;
     }
     if (err == hipSuccess && debug) {
-      const nx_status dst = debug_check(a, s, st);
+      const nx_status dst = debug_check(a.status, s, nx_stage_name(st));
       if (dst != NX_OK) return dst;
     }
   }
@@ -363,6 +362,10 @@ void* scratch_ptr(hipStream_t s) {
 }
 
 }  // namespace
+
+nx_status nx::debug_status(const uint32_t* status, hipStream_t s, const char* name) {
+  return debug_mode() ? debug_check(status, s, name) : NX_OK;
+}
 
 extern "C" {
 

@@ -185,4 +185,8 @@ hipError_t launch_head_budget(const Args& a, hipStream_t s);
 hipError_t launch_stream_read(const void* src, int64_t rows, int mode, uint32_t* sink,
                               hipStream_t s);
 
+// NX_DEBUG's check of one entry point's launches outside the eviction stages:
+// NX_OK at once unless the mode is on and `s` is not being captured.
+nx_status debug_status(const uint32_t* status, hipStream_t s, const char* name);
+
 }  // namespace nx

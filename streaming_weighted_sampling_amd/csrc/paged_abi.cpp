@@ -1,0 +1,318 @@
+// Host side of the decode-step entry points of include/nexus.h (nx_qk_norm_rope,
+// nx_paged_*): argument validation, workspace carving and launches.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "paged.hpp"
+
+using namespace nx;
+
+namespace {
+
+constexpr int64_t kMaxCacheRows = int64_t(1) << 24;
+constexpr int kMaxChunk = 256;     // blocks per chunk: 64 per wavefront, one lane each
+// Workgroups an attention call is split into: 8 per CU keep every CU's loads in
+// flight and leave the uneven heads of a ragged batch to the hardware's balance.
+constexpr int kTargetGroups = 2048;
+
+int32_t elem_size(int32_t dtype) { return dtype == NX_BF16 ? 2 : 4; }
+bool aligned(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+struct Range {
+  uintptr_t lo, hi;
+};
+Range bytes_at(const void* p, int64_t n) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return {lo, lo + uintptr_t(n)};
+}
+bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// A set of rows as the calls address it.
+struct RowSet {
+  const nx_rows* r;
+  int64_t n, heads, d, esz;
+  int64_t extent() const { return (heads - 1) * r->head_stride + d; }   // elements of one row's heads
+  Range range() const { return bytes_at(r->p, n ? ((n - 1) * r->row_stride + extent()) * esz : 0); }
+};
+
+// Exact for two sets that share a row stride which holds a whole row of each
+// (slices of one fused projection); otherwise by address range.
+bool overlap(const RowSet& a, const RowSet& b) {
+  if (!overlap(a.range(), b.range())) return false;
+  const int64_t rs = a.r->row_stride;
+  if (rs == b.r->row_stride && a.extent() <= rs && b.extent() <= rs) {
+    const int64_t diff = int64_t(reinterpret_cast<uintptr_t>(b.r->p) - reinterpret_cast<uintptr_t>(a.r->p));
+    const int64_t at = ((diff / a.esz) % rs + rs) % rs;
+    return !(at >= a.extent() && at + b.extent() <= rs);
+  }
+  return true;
+}
+bool same_rows(const nx_rows* a, const nx_rows* b) {
+  return a->p == b->p && a->row_stride == b->row_stride && a->head_stride == b->head_stride;
+}
+
+nx_status check_rows(const RowSet& s, bool output) {
+  if (s.r == nullptr || (s.r->p == nullptr && s.n > 0)) return NX_EINVAL;
+  if (s.r->row_stride < 0 || s.r->head_stride < 0) return NX_EINVAL;
+  if (!aligned(s.r->p) || s.r->row_stride * s.esz % 16 || s.r->head_stride * s.esz % 16)
+    return NX_EUNSUPPORTED;
+  if (output) {   // rows of an output must not share memory
+    const bool by_row = (s.heads == 1 || s.r->head_stride >= s.d) && (s.n <= 1 || s.r->row_stride >= s.extent());
+    const bool by_head = (s.n <= 1 || s.r->row_stride >= s.d) &&
+                         (s.heads == 1 || s.r->head_stride >= (s.n - 1) * s.r->row_stride + s.d);
+    if (!by_row && !by_head) return NX_EINVAL;
+  }
+  return NX_OK;
+}
+
+nx_status check_rope(const nx_rope* r, int32_t head_dim) {
+  if (r == nullptr) return NX_OK;
+  if (r->cos_sin == nullptr || r->n_pos < 1 || r->rot_dim < 0 || r->rot_dim > head_dim) return NX_EINVAL;
+  if (r->style != NX_ROPE_HALF && r->style != NX_ROPE_PAIRS) return NX_EINVAL;
+  if (r->rot_dim % 16 || !aligned(r->cos_sin)) return NX_EUNSUPPORTED;
+  return NX_OK;
+}
+
+nx_status check_shape(const nx_paged* c) {
+  if (c == nullptr) return NX_EINVAL;
+  if (c->n_seqs < 1 || c->n_kv_heads < 1 || c->n_q_heads < c->n_kv_heads || c->n_q_heads % c->n_kv_heads)
+    return NX_EINVAL;
+  if (c->n_pages < 1 || c->max_pages < 1 || c->page_blocks < 1) return NX_EINVAL;
+  if (c->dtype != NX_BF16 && c->dtype != NX_F32) return NX_EUNSUPPORTED;
+  if (c->format != NX_CACHE_E4M3 && c->format != NX_CACHE_I8) return NX_EUNSUPPORTED;
+  if (c->head_dim != 64 && c->head_dim != 128) return NX_EUNSUPPORTED;
+  if (c->page_blocks > 1024 || (c->page_blocks & (c->page_blocks - 1))) return NX_EUNSUPPORTED;
+  if (c->n_q_heads / c->n_kv_heads > 256) return NX_EUNSUPPORTED;
+  if (int64_t(c->n_seqs) * c->n_kv_heads > 65535) return NX_EUNSUPPORTED;     // grid y
+  if (int64_t(c->n_pages) * c->page_blocks > INT32_MAX) return NX_EUNSUPPORTED;
+  return NX_OK;
+}
+
+struct CacheRanges {
+  Range r[6];   // codes, scales, tails
+};
+CacheRanges cache_ranges(const nx_paged* c) {
+  const int64_t blocks = int64_t(c->n_pages) * c->page_blocks;
+  const int64_t units = int64_t(c->n_seqs) * c->n_kv_heads;
+  const int64_t codes = blocks * kBlock * c->head_dim;
+  const int64_t tail = units * kBlock * c->head_dim * elem_size(c->dtype);
+  return {{bytes_at(c->k_codes, codes), bytes_at(c->v_codes, codes), bytes_at(c->k_scale, blocks * 4),
+           bytes_at(c->v_scale, blocks * 4), bytes_at(c->k_tail, tail), bytes_at(c->v_tail, tail)}};
+}
+
+nx_status check_cache(const nx_paged* c) {
+  nx_status st = check_shape(c);
+  if (st != NX_OK) return st;
+  if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale || !c->k_tail || !c->v_tail || !c->table ||
+      !c->lens)
+    return NX_EINVAL;
+  if (!aligned(c->k_codes) || !aligned(c->v_codes) || !aligned(c->k_tail) || !aligned(c->v_tail))
+    return NX_EUNSUPPORTED;
+  if (c->workspace == nullptr || c->workspace_bytes < 256) return NX_EWORKSPACE;
+  return NX_OK;
+}
+
+PagedArgs base_args(const nx_paged* c) {
+  PagedArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.c = *c;
+  a.group = c->n_q_heads / c->n_kv_heads;
+  while ((1 << a.page_shift) < c->page_blocks) ++a.page_shift;
+  a.status = static_cast<uint32_t*>(c->workspace);
+  return a;
+}
+
+// How an attention call is cut: query-row tiles, chunks of blocks, splits.
+struct Cut {
+  int32_t tile, n_rt, chunk, n_splits;
+  int64_t slots;         // bound on units * n_rt * n_splits for any smaller max_tokens too
+};
+nx_status make_cut(const nx_paged* c, int64_t max_tokens, int64_t max_q, Cut* out) {
+  if (max_tokens < 0 || max_q < 1) return NX_EINVAL;
+  const int64_t rows = max_q * (c->n_q_heads / c->n_kv_heads);
+  if (max_tokens > kMaxCacheRows || rows > (int64_t(1) << 20)) return NX_EUNSUPPORTED;
+  const int64_t tile = paged_tile_rows(rows, c->dtype);
+  const int64_t n_rt = (rows + tile - 1) / tile;
+  const int64_t work = int64_t(c->n_seqs) * c->n_kv_heads * n_rt;
+  const int64_t blocks = std::max<int64_t>(1, (max_tokens + kBlock - 1) / kBlock);
+  // Equal chunks, a multiple of the four wavefronts' blocks.
+  int64_t chunk = ((work * blocks + kTargetGroups - 1) / kTargetGroups + 3) / 4 * 4;
+  chunk = std::min<int64_t>(chunk, kMaxChunk);
+  const int64_t most = std::max<int64_t>(1, kTargetGroups / work);
+  *out = {int32_t(tile), int32_t(n_rt), int32_t(chunk),
+          int32_t(std::min((blocks + chunk - 1) / chunk, most + 1)),
+          std::min(kTargetGroups + work, work * ((blocks + 3) / 4))};
+  return NX_OK;
+}
+size_t part_ml_bytes(const Cut& k) { return align256(size_t(k.slots) * k.tile * 2 * sizeof(float)); }
+size_t cut_bytes(const nx_paged* c, const Cut& k) {
+  return 256 + part_ml_bytes(k) + size_t(k.slots) * k.tile * c->head_dim * sizeof(float);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t nx_paged_workspace_bytes(const nx_paged* cache, int32_t max_tokens, int32_t max_q) {
+  Cut k;
+  if (check_shape(cache) != NX_OK || make_cut(cache, max_tokens, max_q, &k) != NX_OK) return 0;
+  return cut_bytes(cache, k);
+}
+
+nx_status nx_qk_norm_rope(const nx_desc* desc, const nx_rope* rope, int32_t n_rows, const nx_rows* q,
+                          const nx_rows* out_q, const void* q_weight, const nx_rows* k,
+                          const nx_rows* out_k, const void* k_weight, float eps) {
+  if (desc == nullptr || n_rows < 0) return NX_EINVAL;
+  if (desc->n_kv_heads < 1 || desc->n_q_heads < 1) return NX_EINVAL;
+  if (desc->dtype != NX_BF16 && desc->dtype != NX_F32) return NX_EUNSUPPORTED;
+  if (desc->head_dim != 64 && desc->head_dim != 128) return NX_EUNSUPPORTED;
+  if (!std::isfinite(eps) || eps < 0.f) return NX_EINVAL;
+  if ((k == nullptr) != (out_k == nullptr) || (k == nullptr && k_weight != nullptr)) return NX_EINVAL;
+  nx_status st = check_rope(rope, desc->head_dim);
+  if (st != NX_OK) return st;
+  const int64_t esz = elem_size(desc->dtype), d = desc->head_dim;
+  const RowSet sq{q, n_rows, desc->n_q_heads, d, esz}, soq{out_q, n_rows, desc->n_q_heads, d, esz};
+  const RowSet sk{k, n_rows, desc->n_kv_heads, d, esz}, sok{out_k, n_rows, desc->n_kv_heads, d, esz};
+  if ((st = check_rows(sq, false)) != NX_OK || (st = check_rows(soq, true)) != NX_OK) return st;
+  if (!same_rows(q, out_q) && overlap(sq, soq)) return NX_EALIAS;
+  if (k != nullptr) {
+    if ((st = check_rows(sk, false)) != NX_OK || (st = check_rows(sok, true)) != NX_OK) return st;
+    if (!same_rows(k, out_k) && overlap(sk, sok)) return NX_EALIAS;
+    if (overlap(soq, sk) || overlap(soq, sok) || overlap(sok, sq)) return NX_EALIAS;
+  }
+  if (!aligned(q_weight) || !aligned(k_weight)) return NX_EUNSUPPORTED;
+  if (desc->workspace == nullptr || desc->workspace_bytes < 256) return NX_EWORKSPACE;
+  if (n_rows == 0) return NX_OK;
+  NormArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if (rope != nullptr) a.rope = *rope;
+  a.in[0] = *q;
+  a.out[0] = *out_q;
+  a.weight[0] = q_weight;
+  a.heads[0] = desc->n_q_heads;
+  if (k != nullptr) {
+    a.in[1] = *k;
+    a.out[1] = *out_k;
+    a.weight[1] = k_weight;
+    a.heads[1] = desc->n_kv_heads;
+  }
+  a.n_rows = n_rows;
+  a.head_dim = desc->head_dim;
+  a.dtype = desc->dtype;
+  a.eps = eps;
+  a.status = static_cast<uint32_t*>(desc->workspace);
+  hipStream_t s = static_cast<hipStream_t>(desc->stream);
+  if (launch_norm_rope(a, s) != hipSuccess) return NX_EHIP;
+  return debug_status(a.status, s, "qk_norm_rope");
+}
+
+nx_status nx_paged_append(const nx_paged* cache, const nx_rope* rope, const nx_rows* k, const nx_rows* v,
+                          int32_t n_rows, const int32_t* new_start, const int32_t* head_new,
+                          int32_t max_new, int32_t* lens_out) {
+  nx_status st = check_cache(cache);
+  if (st != NX_OK) return st;
+  if (n_rows < 0 || max_new < 0 || max_new > kMaxCacheRows) return NX_EINVAL;
+  if (new_start == nullptr && int64_t(cache->n_seqs) * max_new > n_rows) return NX_EINVAL;
+  if ((st = check_rope(rope, cache->head_dim)) != NX_OK) return st;
+  const int64_t esz = elem_size(cache->dtype), d = cache->head_dim;
+  const RowSet sk{k, n_rows, cache->n_kv_heads, d, esz}, sv{v, n_rows, cache->n_kv_heads, d, esz};
+  if ((st = check_rows(sk, false)) != NX_OK || (st = check_rows(sv, false)) != NX_OK) return st;
+  const CacheRanges cr = cache_ranges(cache);
+  const int64_t units = int64_t(cache->n_seqs) * cache->n_kv_heads;
+  const Range lens = bytes_at(cache->lens, units * 4);
+  const Range lout = bytes_at(lens_out != nullptr ? lens_out : cache->lens, units * 4);
+  const Range ins[] = {sk.range(), sv.range(), bytes_at(cache->table, units * cache->max_pages * 4)};
+  for (int i = 0; i < 6; ++i) {
+    for (int j = i + 1; j < 6; ++j)
+      if (overlap(cr.r[i], cr.r[j])) return NX_EALIAS;
+    for (const Range& x : ins)
+      if (overlap(cr.r[i], x)) return NX_EALIAS;
+    if (overlap(cr.r[i], lens) || overlap(cr.r[i], lout)) return NX_EALIAS;
+  }
+  for (const Range& x : ins)
+    if (overlap(lout, x)) return NX_EALIAS;
+  if (lout.lo != lens.lo && overlap(lout, lens)) return NX_EALIAS;
+  PagedArgs a = base_args(cache);
+  if (rope != nullptr) a.rope = *rope;
+  a.k = *k;
+  a.v = *v;
+  a.n_rows = n_rows;
+  a.max_new = max_new;
+  a.start = new_start;
+  a.head_new = head_new;
+  a.lens_out = lens_out != nullptr ? lens_out : cache->lens;
+  hipStream_t s = static_cast<hipStream_t>(cache->stream);
+  if (launch_paged_append(a, s) != hipSuccess) return NX_EHIP;
+  return debug_status(a.status, s, "paged_append");
+}
+
+nx_status nx_paged_attn(const nx_paged* cache, const nx_rows* q, const nx_rows* out, int32_t n_rows,
+                        const int32_t* q_start, int32_t max_tokens, int32_t max_q, float scale,
+                        float* out_lse) {
+  nx_status st = check_cache(cache);
+  if (st != NX_OK) return st;
+  if (n_rows < 0 || !std::isfinite(scale) || scale < 0.f) return NX_EINVAL;
+  if (q_start == nullptr && int64_t(cache->n_seqs) * max_q > n_rows) return NX_EINVAL;
+  Cut cut;
+  if ((st = make_cut(cache, max_tokens, max_q, &cut)) != NX_OK) return st;
+  const int64_t esz = elem_size(cache->dtype), d = cache->head_dim;
+  const RowSet sq{q, n_rows, cache->n_q_heads, d, esz}, so{out, n_rows, cache->n_q_heads, d, esz};
+  if ((st = check_rows(sq, false)) != NX_OK || (st = check_rows(so, true)) != NX_OK) return st;
+  if (overlap(sq, so)) return NX_EALIAS;
+  const CacheRanges cr = cache_ranges(cache);
+  const Range lse = bytes_at(out_lse, out_lse != nullptr ? int64_t(n_rows) * cache->n_q_heads * 4 : 0);
+  for (const Range& x : cr.r)
+    if (overlap(so.range(), x) || overlap(lse, x)) return NX_EALIAS;
+  if (overlap(lse, sq.range()) || overlap(lse, so.range())) return NX_EALIAS;
+  if (cache->workspace_bytes < cut_bytes(cache, cut)) return NX_EWORKSPACE;
+  PagedArgs a = base_args(cache);
+  a.q = *q;
+  a.out = *out;
+  a.n_rows = n_rows;
+  a.start = q_start;
+  a.max_q = max_q;
+  a.n_rt = cut.n_rt;
+  a.n_splits = cut.n_splits;
+  a.chunk = cut.chunk;
+  a.scale_log2 = float((scale > 0.f ? double(scale) : 1.0 / std::sqrt(double(d))) * 1.4426950408889634);
+  a.lse = out_lse;
+  char* ws = static_cast<char*>(cache->workspace) + 256;
+  a.part_ml = reinterpret_cast<float*>(ws);
+  a.part_o = reinterpret_cast<float*>(ws + part_ml_bytes(cut));
+  hipStream_t s = static_cast<hipStream_t>(cache->stream);
+  if (launch_paged_attn(a, s) != hipSuccess) return NX_EHIP;
+  return debug_status(a.status, s, "paged_attn");
+}
+
+nx_status nx_paged_gather(const nx_paged* cache, int32_t max_tokens, void* out_k, void* out_v,
+                          int64_t out_seq_stride, int64_t out_head_stride) {
+  nx_status st = check_cache(cache);
+  if (st != NX_OK) return st;
+  if (max_tokens < 0 || max_tokens > kMaxCacheRows || out_k == nullptr || out_v == nullptr) return NX_EINVAL;
+  const int64_t d = cache->head_dim, esz = elem_size(cache->dtype), hk = cache->n_kv_heads;
+  const int64_t rows = int64_t(max_tokens) * d;
+  if (out_head_stride < rows || out_seq_stride < (hk - 1) * out_head_stride + rows) {
+    if (!(cache->n_seqs == 1 && out_head_stride >= rows)) return NX_EINVAL;
+  }
+  if (!aligned(out_k) || !aligned(out_v) || out_seq_stride * esz % 16 || out_head_stride * esz % 16)
+    return NX_EUNSUPPORTED;
+  const int64_t n = ((cache->n_seqs - 1) * out_seq_stride + (hk - 1) * out_head_stride + rows) * esz;
+  const Range ok = bytes_at(out_k, n), ov = bytes_at(out_v, n);
+  const CacheRanges cr = cache_ranges(cache);
+  if (overlap(ok, ov)) return NX_EALIAS;
+  for (const Range& x : cr.r)
+    if (overlap(ok, x) || overlap(ov, x)) return NX_EALIAS;
+  if (max_tokens == 0) return NX_OK;
+  PagedArgs a = base_args(cache);
+  a.max_tokens = max_tokens;
+  a.out_k = out_k;
+  a.out_v = out_v;
+  a.out_seq_stride = out_seq_stride;
+  a.out_head_stride = out_head_stride;
+  hipStream_t s = static_cast<hipStream_t>(cache->stream);
+  if (launch_paged_gather(a, s) != hipSuccess) return NX_EHIP;
+  return debug_status(a.status, s, "paged_gather");
+}
+
+}  // extern "C"

@@ -1,0 +1,325 @@
+"""Torch-facing binding of the decode-step operators: checks and marshalling, no arithmetic.
+
+Between two eviction events each new token is normed and rotated
+(nx_qk_norm_rope), appended to a paged 8-bit cache (nx_paged_append) and attended
+over it (nx_paged_attn); nx_paged_gather reads the rows back for the next event.
+The functions mirror include/nexus.h; shapes and the element type come from the
+NexusConfig of the eviction calls.  Work is enqueued on the current stream of
+the tensors' device (or the given stream).
+"""
+
+import ctypes
+from dataclasses import dataclass, field
+
+import torch
+
+from ._lib import (NX_CACHE_BLOCK, NX_CACHE_E4M3, NX_CACHE_I8, NX_ROPE_HALF, NX_ROPE_PAIRS, NxPaged,
+                   NxRope, NxRows, check, load)
+from .api import _DTYPES, NexusConfig
+
+_FORMATS = {torch.float8_e4m3fn: NX_CACHE_E4M3, torch.int8: NX_CACHE_I8}
+_NAMES = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+
+
+def _tensor(t, name, shape, dtype, device=None):
+    """Checks a whole contiguous tensor; returns its address."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected contiguous {tuple(shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def _opt(t, name, shape, dtype, device):
+    return None if t is None else _tensor(t, name, shape, dtype, device)
+
+
+def _rows(cfg, t, name, heads, device, n_rows=None):
+    """NxRows of a [rows, heads, head_dim] tensor with any row and head strides."""
+    if t.dtype != cfg.dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {cfg.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != cfg.head_dim or \
+            (n_rows is not None and shape[0] != n_rows):
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected "
+                         f"[{'rows' if n_rows is None else n_rows}, {heads}, {cfg.head_dim}]")
+    s0, s1, s2 = t.stride()
+    if s2 != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return NxRows(t.data_ptr(), s0, s1)
+
+
+def _call(device, stream, set_stream, fn):
+    """Runs fn with `device` current and set_stream(handle) done."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {device}")
+    if torch.cuda.current_device() == device.index:
+        set_stream((stream or torch.cuda.current_stream()).cuda_stream)
+        return fn()
+    with torch.cuda.device(device):
+        set_stream((stream or torch.cuda.current_stream()).cuda_stream)
+        return fn()
+
+
+@dataclass
+class Rope:
+    """Rotation table: cos_sin [n_pos, rot_dim] float32 (rot_dim / 2 cosines, then the
+    sines); pairs=False turns elements (i, i + rot_dim / 2), pairs=True (2 i, 2 i + 1)."""
+    cos_sin: torch.Tensor
+    pairs: bool = False
+
+    def __post_init__(self):
+        t = self.cos_sin
+        if t.dim() != 2 or t.dtype != torch.float32 or not t.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous float32 [n_pos, rot_dim] tensor")
+
+    def _struct(self, positions, n_rows, device):
+        t = self.cos_sin
+        if t.device != device:
+            raise ValueError(f"cos_sin is on {t.device}, expected {device}")
+        return NxRope(t.data_ptr(), _opt(positions, "positions", (n_rows,), torch.int32, device),
+                      t.shape[0], t.shape[1], NX_ROPE_PAIRS if self.pairs else NX_ROPE_HALF)
+
+
+def rope_table(n_pos, rot_dim, base=10000.0, *, inv_freq=None, first=0, device="cuda"):
+    """cos_sin table of positions first .. first + n_pos - 1, angles in float64.
+
+    inv_freq: the rot_dim / 2 frequencies (default base ** (-2 i / rot_dim))."""
+    if inv_freq is None:
+        i = torch.arange(rot_dim // 2, dtype=torch.float64, device=device)
+        inv_freq = float(base) ** (-2.0 * i / rot_dim)
+    inv_freq = torch.as_tensor(inv_freq, dtype=torch.float64, device=device)
+    pos = torch.arange(first, first + n_pos, dtype=torch.float64, device=device)
+    angle = pos[:, None] * inv_freq
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+@dataclass
+class PagedCache:
+    """The arrays of one paged 8-bit cache (layouts in include/nexus.h, nx_paged).
+
+    The format is the dtype of the codes (float8_e4m3fn or int8).  table and
+    lens may be rewritten between calls (in place); the arrays themselves stay."""
+    cfg: NexusConfig
+    k_codes: torch.Tensor      # [n_pages, page_blocks, 32, D]
+    v_codes: torch.Tensor      # [n_pages, page_blocks, 4, D, 8]
+    k_scale: torch.Tensor      # [n_pages, page_blocks] float32
+    v_scale: torch.Tensor
+    k_tail: torch.Tensor       # [n_seqs, n_kv_heads, 32, D] of cfg.dtype
+    v_tail: torch.Tensor       # [n_seqs, n_kv_heads, 4, D, 8]
+    table: torch.Tensor        # [n_seqs, n_kv_heads, max_pages] int32
+    lens: torch.Tensor         # [n_seqs, n_kv_heads] int32
+    _c: NxPaged = field(init=False, repr=False, compare=False, default=None)
+
+    def __post_init__(self):
+        cfg, d, hk = self.cfg, self.cfg.head_dim, self.cfg.n_kv_heads
+        if self.k_codes.dtype not in _FORMATS:
+            raise TypeError(f"k_codes: dtype {self.k_codes.dtype}, expected one of {list(_FORMATS)}")
+        if self.k_codes.dim() != 4 or self.table.dim() != 3:
+            raise ValueError("k_codes must be [n_pages, page_blocks, 32, head_dim], table "
+                             "[n_seqs, n_kv_heads, max_pages]")
+        n_pages, blocks = self.k_codes.shape[:2]
+        n_seqs, _, max_pages = self.table.shape
+        dev, f8 = self.k_codes.device, self.k_codes.dtype
+        self.device, self.n_seqs = dev, n_seqs
+        self.capacity = max_pages * blocks * NX_CACHE_BLOCK      # rows that a head's table can hold
+        c = NxPaged()
+        c.n_seqs, c.n_q_heads, c.n_kv_heads, c.head_dim = n_seqs, cfg.n_q_heads, hk, d
+        c.dtype, c.format = _DTYPES.get(cfg.dtype, 99), _FORMATS[f8]
+        c.page_blocks, c.n_pages, c.max_pages = blocks, n_pages, max_pages
+        c.k_codes = _tensor(self.k_codes, "k_codes", (n_pages, blocks, NX_CACHE_BLOCK, d), f8)
+        c.v_codes = _tensor(self.v_codes, "v_codes", (n_pages, blocks, 4, d, 8), f8, dev)
+        c.k_scale = _tensor(self.k_scale, "k_scale", (n_pages, blocks), torch.float32, dev)
+        c.v_scale = _tensor(self.v_scale, "v_scale", (n_pages, blocks), torch.float32, dev)
+        c.k_tail = _tensor(self.k_tail, "k_tail", (n_seqs, hk, NX_CACHE_BLOCK, d), cfg.dtype, dev)
+        c.v_tail = _tensor(self.v_tail, "v_tail", (n_seqs, hk, 4, d, 8), cfg.dtype, dev)
+        c.table = _tensor(self.table, "table", (n_seqs, hk, max_pages), torch.int32, dev)
+        c.lens = _tensor(self.lens, "lens", (n_seqs, hk), torch.int32, dev)
+        self._c = c
+
+    def _struct(self, cfg, workspace):
+        if cfg is not self.cfg and cfg != self.cfg:
+            raise ValueError("the cache was made for another configuration")
+        if workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError(f"the workspace must be contiguous on {self.device}")
+        # A copy: calls from several threads share the cache object.
+        c = NxPaged.from_buffer_copy(self._c)
+        c.workspace = workspace.data_ptr()
+        c.workspace_bytes = workspace.numel() * workspace.element_size()
+        return c
+
+
+def new_paged_cache(cfg, n_seqs, n_pages, max_pages, *, fmt="e4m3", page_blocks=4, device="cuda"):
+    """An empty cache: zero lengths, and a table whose entries are -1 (no page) until the
+    caller hands pages out."""
+    if fmt not in _NAMES:
+        raise ValueError(f"fmt {fmt!r}, expected one of {sorted(_NAMES)}")
+    d, hk = cfg.head_dim, cfg.n_kv_heads
+
+    def zeros(*shape, dtype):
+        return torch.zeros(shape, dtype=dtype, device=device)
+
+    codes = [zeros(n_pages, page_blocks, NX_CACHE_BLOCK * d, dtype=torch.uint8).view(_NAMES[fmt])
+             for _ in range(2)]
+    return PagedCache(
+        cfg, codes[0].view(n_pages, page_blocks, NX_CACHE_BLOCK, d),
+        codes[1].view(n_pages, page_blocks, 4, d, 8),
+        zeros(n_pages, page_blocks, dtype=torch.float32), zeros(n_pages, page_blocks, dtype=torch.float32),
+        zeros(n_seqs, hk, NX_CACHE_BLOCK, d, dtype=cfg.dtype), zeros(n_seqs, hk, 4, d, 8, dtype=cfg.dtype),
+        zeros(n_seqs, hk, max_pages, dtype=torch.int32) - 1, zeros(n_seqs, hk, dtype=torch.int32))
+
+
+def paged_workspace_bytes(cfg, cache, max_tokens, max_q=1):
+    c = NxPaged.from_buffer_copy(cache._c)
+    n = load().nx_paged_workspace_bytes(ctypes.byref(c), max_tokens, max_q)
+    if n == 0:
+        raise ValueError("invalid shape for the workspace query")
+    return n
+
+
+def new_paged_workspace(cfg, cache, max_tokens, max_q=1):
+    """Zero-filled workspace of the nx_paged_* calls (nx_read_device_status reads its status)."""
+    return torch.zeros(paged_workspace_bytes(cfg, cache, max_tokens, max_q), dtype=torch.uint8,
+                       device=cache.device)
+
+
+def nx_qk_norm_rope(cfg, q, k=None, *, workspace, q_weight=None, k_weight=None, eps=1e-6, rope=None,
+                    positions=None, out_q=None, out_k=None, stream=None):
+    """Root-mean-square norm of every head of q [rows, n_q_heads, D] and k
+    [rows, n_kv_heads, D], then the rotation; returns (out_q, out_k).
+
+    A side without a weight is rotated only; rope None: no rotation.  Outputs
+    may be views with other strides (a query window, a cache's append rows) or
+    the inputs themselves."""
+    dev, n = q.device, q.shape[0]
+    rq = _rows(cfg, q, "q", cfg.n_q_heads, dev)
+    if out_q is None:
+        out_q = torch.empty(n, cfg.n_q_heads, cfg.head_dim, dtype=cfg.dtype, device=dev)
+    roq = _rows(cfg, out_q, "out_q", cfg.n_q_heads, dev, n)
+    rk = rok = None
+    if k is not None:
+        rk = _rows(cfg, k, "k", cfg.n_kv_heads, dev, n)
+        if out_k is None:
+            out_k = torch.empty(n, cfg.n_kv_heads, cfg.head_dim, dtype=cfg.dtype, device=dev)
+        rok = _rows(cfg, out_k, "out_k", cfg.n_kv_heads, dev, n)
+    elif out_k is not None:
+        raise ValueError("out_k without k")
+    wq = _opt(q_weight, "q_weight", (cfg.head_dim,), cfg.dtype, dev)
+    wk = _opt(k_weight, "k_weight", (cfg.head_dim,), cfg.dtype, dev)
+    if rope is None and positions is not None:
+        raise ValueError("positions without rope")
+    r = None if rope is None else rope._struct(positions, n, dev)
+    if workspace.device != dev:
+        raise ValueError(f"the workspace must be on {dev}")
+    d = cfg.desc(workspace)
+    lib = load()
+
+    def set_stream(s):
+        d.stream = s
+
+    check(_call(dev, stream, set_stream,
+                lambda: lib.nx_qk_norm_rope(d, r, n, rq, roq, wq, rk, rok, wk, eps)), "nx_qk_norm_rope")
+    return out_q, out_k
+
+
+def nx_paged_append(cfg, cache, k, v, *, workspace, max_new=None, new_start=None, head_new=None,
+                    rope=None, positions=None, lens_out=None, stream=None):
+    """Appends rows k, v [rows, n_kv_heads, D] (K rotated by `rope`) to every sequence.
+
+    new_start: int32 [n_seqs + 1] first rows of the sequences (None: max_new rows each,
+    default rows // n_seqs); head_new: int32 [n_seqs, n_kv_heads] rows each head takes of
+    its sequence's; lens_out: int32 [n_seqs, n_kv_heads] (None: cache.lens is advanced)."""
+    dev, n, hk = cache.device, k.shape[0], cfg.n_kv_heads
+    rk = _rows(cfg, k, "k", hk, dev)
+    rv = _rows(cfg, v, "v", hk, dev, n)
+    if max_new is None:
+        if new_start is not None:
+            raise ValueError("new_start needs max_new")
+        if n % cache.n_seqs:
+            raise ValueError(f"{n} rows do not divide into {cache.n_seqs} sequences")
+        max_new = n // cache.n_seqs
+    ns = _opt(new_start, "new_start", (cache.n_seqs + 1,), torch.int32, dev)
+    hn = _opt(head_new, "head_new", (cache.n_seqs, hk), torch.int32, dev)
+    lo = _opt(lens_out, "lens_out", (cache.n_seqs, hk), torch.int32, dev)
+    if rope is None and positions is not None:
+        raise ValueError("positions without rope")
+    r = None if rope is None else rope._struct(positions, n, dev)
+    c = cache._struct(cfg, workspace)
+    lib = load()
+
+    def set_stream(s):
+        c.stream = s
+
+    check(_call(dev, stream, set_stream,
+                lambda: lib.nx_paged_append(c, r, rk, rv, n, ns, hn, max_new, lo)), "nx_paged_append")
+
+
+def nx_paged_attn(cfg, cache, q, *, workspace, max_tokens, max_q=None, q_start=None, scale=None,
+                  out=None, out_lse=None, stream=None):
+    """Attention of q [rows, n_q_heads, D] over the cache; returns out of q's shape.
+
+    q_start: int32 [n_seqs + 1] first query rows of the sequences (None: max_q each, default
+    rows // n_seqs); max_tokens: the expected longest head (any value is correct, and the
+    workspace must have been made for at least it); out_lse: float32 [rows, n_q_heads]."""
+    dev, n = cache.device, q.shape[0]
+    rq = _rows(cfg, q, "q", cfg.n_q_heads, dev)
+    if out is None:
+        out = torch.empty(n, cfg.n_q_heads, cfg.head_dim, dtype=cfg.dtype, device=dev)
+    ro = _rows(cfg, out, "out", cfg.n_q_heads, dev, n)
+    if max_q is None:
+        if q_start is not None:
+            raise ValueError("q_start needs max_q")
+        if n % cache.n_seqs:
+            raise ValueError(f"{n} rows do not divide into {cache.n_seqs} sequences")
+        max_q = n // cache.n_seqs
+    if scale is not None and not scale > 0:
+        raise ValueError("scale must be positive")
+    qs = _opt(q_start, "q_start", (cache.n_seqs + 1,), torch.int32, dev)
+    lse = _opt(out_lse, "out_lse", (n, cfg.n_q_heads), torch.float32, dev)
+    c = cache._struct(cfg, workspace)
+    lib = load()
+
+    def set_stream(s):
+        c.stream = s
+
+    check(_call(dev, stream, set_stream,
+                lambda: lib.nx_paged_attn(c, rq, ro, n, qs, max_tokens, max_q, scale or 0.0, lse)),
+          "nx_paged_attn")
+    return out
+
+
+def nx_paged_gather(cfg, cache, *, workspace, max_tokens, out_k=None, out_v=None, stream=None):
+    """The cached rows as [n_seqs, n_kv_heads, >= max_tokens, D] tensors (rows past a head's
+    length are left as they were; new outputs are zero-filled); returns (out_k, out_v)."""
+    dev, hk, d = cache.device, cfg.n_kv_heads, cfg.head_dim
+    shape = (cache.n_seqs, hk, max_tokens, d)
+    if out_k is None:
+        out_k = torch.zeros(shape, dtype=cfg.dtype, device=dev)
+    if out_v is None:
+        out_v = torch.zeros_like(out_k)
+    for t, name in ((out_k, "out_k"), (out_v, "out_v")):
+        if t.dtype != cfg.dtype:
+            raise TypeError(f"{name}: dtype {t.dtype}, expected {cfg.dtype}")
+        if t.dim() != 4 or t.shape[:2] != shape[:2] or t.shape[2] < max_tokens or t.shape[3] != d:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+        if t.stride(3) != 1 or t.stride(2) != d or t.device != dev:
+            raise ValueError(f"{name}: rows must be contiguous on {dev}")
+    if out_k.stride() != out_v.stride():
+        raise ValueError("out_k and out_v must share their strides")
+    c = cache._struct(cfg, workspace)
+    lib = load()
+
+    def set_stream(s):
+        c.stream = s
+
+    check(_call(dev, stream, set_stream,
+                lambda: lib.nx_paged_gather(c, max_tokens, out_k.data_ptr(), out_v.data_ptr(),
+                                            out_k.stride(0), out_k.stride(1))), "nx_paged_gather")
+    return out_k, out_v

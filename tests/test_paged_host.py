@@ -1,0 +1,231 @@
+"""Host-side validation of the decode-step entry points: bad arguments are refused
+before anything reaches a GPU (no launch is made here)."""
+
+import ctypes
+import os
+import subprocess
+
+import pytest
+import torch
+
+import streaming_weighted_sampling_amd as nx
+from streaming_weighted_sampling_amd import _lib
+from streaming_weighted_sampling_amd._lib import NxDesc, NxPaged, NxRope, NxRows
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 1 << 40          # never dereferenced
+GB = 1 << 32
+EINVAL, EALIAS, EWORK, EUNSUP = (_lib.NX_EINVAL, _lib.NX_EALIAS, _lib.NX_EWORKSPACE,
+                                 _lib.NX_EUNSUPPORTED)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_lib.LIB_PATH):
+        pytest.skip("libnexus.so not built")
+    return _lib.load()
+
+
+def _cache(**kw):
+    c = NxPaged()
+    c.n_seqs, c.n_q_heads, c.n_kv_heads, c.head_dim = 4, 32, 8, 128
+    c.dtype, c.format, c.page_blocks, c.n_pages, c.max_pages = _lib.NX_BF16, _lib.NX_CACHE_E4M3, 4, 1024, 16
+    for i, name in enumerate(("k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail", "table", "lens",
+                              "workspace")):
+        setattr(c, name, FAKE + i * GB)
+    c.workspace_bytes = 0        # below 256: every valid call ends with NX_EWORKSPACE, unlaunched
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+def _r(slot, row=8 * 128, head=128):
+    return NxRows(FAKE + slot * GB, row, head)
+
+
+def test_struct_layouts_match_c(tmp_path):
+    src = tmp_path / "layout.c"
+    names = {"nx_paged": NxPaged, "nx_rope": NxRope, "nx_rows": NxRows}
+    lines = [f'printf("{n} %zu\\n", sizeof({n}));' for n in names]
+    lines += [f'printf("{n}.{f} %zu\\n", offsetof({n}, {f}));' for n, t in names.items() for f, _ in t._fields_]
+    src.write_text("#include <stddef.h>\n#include <stdio.h>\n#include \"nexus.h\"\nint main(void) {\n"
+                   + "\n".join(lines) + "\nreturn 0;\n}\n")
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-std=c99", f"-I{os.path.join(ROOT, 'include')}", str(src), "-o", str(exe)],
+                   check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout
+    for line in out.splitlines():
+        name, n = line.rsplit(" ", 1)
+        t, _, f = name.partition(".")
+        assert int(n) == (getattr(names[t], f).offset if f else ctypes.sizeof(names[t])), name
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n_seqs=0), EINVAL), (dict(n_q_heads=30), EINVAL), (dict(n_kv_heads=0), EINVAL),
+    (dict(n_pages=0), EINVAL), (dict(max_pages=0), EINVAL), (dict(page_blocks=0), EINVAL),
+    (dict(page_blocks=3), EUNSUP), (dict(page_blocks=2048), EUNSUP), (dict(head_dim=96), EUNSUP),
+    (dict(dtype=2), EUNSUP), (dict(format=2), EUNSUP), (dict(n_seqs=9000), EUNSUP),
+    (dict(n_pages=1 << 30, page_blocks=4), EUNSUP), (dict(n_q_heads=8 * 257), EUNSUP),
+    (dict(k_codes=None), EINVAL), (dict(v_codes=None), EINVAL), (dict(k_scale=None), EINVAL),
+    (dict(v_tail=None), EINVAL), (dict(table=None), EINVAL), (dict(lens=None), EINVAL),
+    (dict(k_codes=FAKE + 8), EUNSUP), (dict(v_tail=FAKE + 2), EUNSUP), (dict(workspace=None), EWORK),
+    (dict(), EWORK)])
+def test_cache_descriptions(lib, kw, code):
+    c = _cache(**kw)
+    assert lib.nx_paged_append(c, None, _r(20), _r(21), 4, None, None, 1, None) == code
+    assert lib.nx_paged_attn(c, _r(20, 4096), _r(21, 4096), 4, None, 100, 1, 0.0, None) == code
+    assert lib.nx_paged_gather(c, 100, FAKE + 30 * GB, FAKE + 31 * GB, 8 * 12800, 12800) == code
+    assert lib.nx_paged_append(None, None, _r(20), _r(21), 4, None, None, 1, None) == EINVAL
+
+
+def _ws(**kw):
+    return _cache(workspace_bytes=256, **kw)
+
+
+def test_append_arguments(lib):
+    def call(c=None, rope=None, k=_r(20), v=_r(21), n=4, start=None, head_new=None, most=1, out=None):
+        return lib.nx_paged_append(c or _ws(), rope, k, v, n, start, head_new, most, out)
+    assert call(k=None) == EINVAL
+    assert call(k=NxRows(None, 1024, 128)) == EINVAL
+    assert call(n=-1) == EINVAL
+    assert call(most=-1) == EINVAL
+    assert call(most=2) == EINVAL                         # 4 sequences x 2 rows > 4 rows
+    assert call(k=_r(20, row=1028)) == EUNSUP             # not a multiple of 16 bytes
+    assert call(v=_r(20, head=-128)) == EINVAL
+    assert call(k=NxRows(FAKE + 20 * GB + 8, 1024, 128)) == EUNSUP
+    assert call(k=_r(0)) == EALIAS                        # new rows inside the codes
+    assert call(v=_r(5)) == EALIAS
+    assert call(c=_ws(v_codes=FAKE + 4096)) == EALIAS     # codes overlap each other
+    assert call(c=_ws(k_scale=FAKE + 4096)) == EALIAS
+    assert call(out=FAKE + 7 * GB + 4) == EALIAS          # shifted against lens
+    assert call(out=FAKE + 6 * GB) == EALIAS              # the table
+    for kw, code in ((dict(rot_dim=24), EUNSUP), (dict(rot_dim=144), EINVAL), (dict(rot_dim=-16), EINVAL),
+                     (dict(n_pos=0), EINVAL), (dict(style=2), EINVAL), (dict(cos_sin=None), EINVAL),
+                     (dict(cos_sin=FAKE + 4), EUNSUP)):
+        f = dict(cos_sin=FAKE + 40 * GB, positions=None, n_pos=10, rot_dim=64, style=0) | kw
+        rope = NxRope(f["cos_sin"], f["positions"], f["n_pos"], f["rot_dim"], f["style"])
+        assert call(rope=rope) == code, kw
+
+
+def test_attention_arguments(lib):
+    def call(c=None, q=_r(20, 4096), o=_r(21, 4096), n=4, start=None, t=100, m=1, scale=0.0, lse=None):
+        return lib.nx_paged_attn(c or _ws(), q, o, n, start, t, m, scale, lse)
+    assert call(m=0) == EINVAL
+    assert call(m=2) == EINVAL                            # more rows than there are
+    assert call(t=-1) == EINVAL
+    assert call(t=1 << 25) == EUNSUP
+    assert call(scale=-1.0) == EINVAL
+    assert call(scale=float("nan")) == EINVAL
+    assert call(o=_r(20, 4096)) == EALIAS
+    assert call(o=_r(21, 128)) == EINVAL                  # output rows on top of each other
+    assert call(o=_r(21, 4096, 0)) == EINVAL
+    assert call(o=_r(4, 4096)) == EALIAS                  # into the tail
+    assert call(lse=FAKE + 21 * GB) == EALIAS
+    assert call() == EWORK                                # 256 bytes hold no partials
+    # slices of one projection do not overlap: the call gets as far as the workspace
+    one = NxRows(FAKE + 20 * GB, 3 * 4096, 128)
+    two = NxRows(FAKE + 20 * GB + 2 * 4096, 3 * 4096, 128)
+    assert call(q=one, o=two) == EWORK
+    assert call(q=one, o=NxRows(FAKE + 20 * GB + 4096, 3 * 4096, 128)) == EALIAS
+
+
+def test_gather_arguments(lib):
+    def call(c=None, t=100, k=FAKE + 30 * GB, v=FAKE + 31 * GB, ss=8 * 12800, hs=12800):
+        return lib.nx_paged_gather(c or _ws(), t, k, v, ss, hs)
+    assert call(k=None) == EINVAL
+    assert call(t=-1) == EINVAL
+    assert call(t=101) == EINVAL                          # head stride below max_tokens rows
+    assert call(ss=12800) == EINVAL
+    assert call(v=FAKE + 30 * GB + 4096) == EALIAS
+    assert call(k=FAKE) == EALIAS
+    assert call(k=FAKE + 30 * GB + 8) == EUNSUP
+    assert call(t=0, hs=0, ss=0) == _lib.NX_OK            # nothing to do
+
+
+def test_norm_rope_arguments(lib):
+    def desc(**kw):
+        d = NxDesc()
+        d.n_q_heads, d.n_kv_heads, d.head_dim, d.window, d.dtype = 32, 8, 128, 1, _lib.NX_BF16
+        d.workspace, d.workspace_bytes = FAKE, 256
+        for k, v in kw.items():
+            setattr(d, k, v)
+        return d
+
+    def call(d=None, n=4, q=_r(20, 4096), oq=_r(21, 4096), wq=None, k=None, ok=None, wk=None, eps=1e-6):
+        return lib.nx_qk_norm_rope(d or desc(), None, n, q, oq, wq, k, ok, wk, eps)
+    assert lib.nx_qk_norm_rope(None, None, 4, _r(20), _r(21), None, None, None, None, 1e-6) == EINVAL
+    assert call(n=-1) == EINVAL
+    assert call(n=0) == _lib.NX_OK
+    assert call(q=None) == EINVAL
+    assert call(eps=-1.0) == EINVAL
+    assert call(eps=float("inf")) == EINVAL
+    assert call(d=desc(dtype=5)) == EUNSUP
+    assert call(d=desc(head_dim=80)) == EUNSUP
+    assert call(d=desc(workspace=None)) == EWORK
+    assert call(k=_r(22)) == EINVAL                       # k without out_k
+    assert call(wk=FAKE) == EINVAL                        # a weight without k
+    assert call(wq=FAKE + 4) == EUNSUP
+    assert call(oq=NxRows(FAKE + 20 * GB + 256, 4096, 128)) == EALIAS
+    assert call(oq=_r(21, 128)) == EINVAL
+    assert call(k=_r(22), ok=_r(21)) == EALIAS            # out_k on out_q
+
+
+def test_workspace_query(lib):
+    c = _cache()
+    small = lib.nx_paged_workspace_bytes(c, 819, 1)
+    assert 256 < small <= lib.nx_paged_workspace_bytes(c, 32768, 1)
+    assert lib.nx_paged_workspace_bytes(c, 32768, 1) <= lib.nx_paged_workspace_bytes(c, 32768, 64)
+    assert lib.nx_paged_workspace_bytes(None, 100, 1) == 0
+    assert lib.nx_paged_workspace_bytes(c, -1, 1) == 0
+    assert lib.nx_paged_workspace_bytes(c, 100, 0) == 0
+    assert lib.nx_paged_workspace_bytes(_cache(head_dim=32), 100, 1) == 0
+
+
+def test_the_binding_checks_tensors():
+    cfg = nx.NexusConfig(4, 2, 64, 1, torch.bfloat16)
+    c = nx.new_paged_cache(cfg, 3, 8, 2, device="cpu")
+    assert c.capacity == 2 * 4 * 32 and (c.table == -1).all() and c.n_seqs == 3
+    ws = torch.zeros(256, dtype=torch.uint8)
+    k = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        nx.nx_paged_append(cfg, c, k, k, workspace=ws)
+    with pytest.raises(TypeError):
+        nx.nx_paged_append(cfg, c, k.float(), k, workspace=ws)
+    with pytest.raises(ValueError, match="shape"):
+        nx.nx_paged_append(cfg, c, k[:, :1], k, workspace=ws)
+    with pytest.raises(ValueError, match="divide"):
+        nx.nx_paged_append(cfg, c, k[:2], k[:2], workspace=ws)
+    with pytest.raises(ValueError, match="contiguous"):
+        nx.nx_paged_append(cfg, c, torch.zeros(3, 2, 128, dtype=torch.bfloat16)[..., ::2], k, workspace=ws)
+    with pytest.raises(ValueError, match="max_new"):
+        nx.nx_paged_append(cfg, c, k, k, workspace=ws, new_start=torch.zeros(4, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        nx.nx_paged_append(cfg, c, k, k, workspace=ws, lens_out=torch.zeros(3, 2))
+    with pytest.raises(ValueError, match="configuration"):
+        nx.nx_paged_append(nx.NexusConfig(8, 2, 64, 1), c, k, k, workspace=ws)
+    with pytest.raises(ValueError, match="positions"):
+        nx.nx_paged_append(cfg, c, k, k, workspace=ws, positions=torch.zeros(3, dtype=torch.int32))
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="scale"):
+        nx.nx_paged_attn(cfg, c, q, workspace=ws, max_tokens=5, scale=0.0)
+    with pytest.raises(ValueError, match="out"):
+        nx.nx_paged_attn(cfg, c, q, workspace=ws, max_tokens=5, out=q[:2])
+    with pytest.raises(ValueError, match="strides"):
+        nx.nx_paged_gather(cfg, c, workspace=ws, max_tokens=5,
+                           out_k=torch.zeros(3, 2, 5, 64, dtype=torch.bfloat16),
+                           out_v=torch.zeros(3, 2, 9, 64, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="out_k"):
+        nx.nx_qk_norm_rope(cfg, q, workspace=ws, out_k=q)
+    with pytest.raises(ValueError):
+        nx.new_paged_cache(cfg, 3, 8, 2, fmt="e5m2", device="cpu")
+    with pytest.raises(ValueError, match="cos_sin"):
+        nx.Rope(torch.zeros(4, 16, dtype=torch.float64))
+    with pytest.raises(ValueError, match="v_codes"):
+        nx.PagedCache(cfg, c.k_codes, c.k_codes, c.k_scale, c.v_scale, c.k_tail, c.v_tail, c.table, c.lens)
+
+
+def test_rope_table_holds_fp64_angles():
+    t = nx.rope_table(5, 8, 100.0, first=100000, device="cpu").double()
+    i = torch.arange(4, dtype=torch.float64)
+    a = torch.arange(100000, 100005, dtype=torch.float64)[:, None] * 100.0 ** (-i / 4)
+    assert torch.allclose(t[:, :4], a.cos(), atol=1e-7) and torch.allclose(t[:, 4:], a.sin(), atol=1e-7)
