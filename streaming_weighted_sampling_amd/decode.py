@@ -1,0 +1,133 @@
+"""Decoding over an 8-bit cache between eviction events: one layer, several sequences.
+
+[Nexus] ("Forget Without Compromise: Nexus Sampling for Streaming KV-Cache
+Eviction Under Fixed Budgets", section 2.1) decodes over the kept rows and evicts
+again whenever the budget is hit.  This driver holds the kept rows in the paged
+8-bit cache: step() norms and rotates one new token per sequence, appends it and
+attends; evict() reads the cache back, runs one nx_evict_batch event over all
+sequences with the last W queries as the window, and refills the cache with the
+kept rows.  Nothing synchronises: row counts, also the heads' different ones under
+per-head budgets, stay on the device.  Marshalling only; every byte of a step
+moves inside libnexus.so.
+"""
+
+import torch
+
+from ._lib import NX_CACHE_BLOCK, NX_HEADS_UNIFORM
+from .api import NexusConfig, make_units, new_workspace, nx_evict_batch, nx_read_device_status
+from .paged import (new_paged_cache, new_paged_workspace, nx_paged_append, nx_paged_attn, nx_paged_gather,
+                    nx_qk_norm_rope)
+
+
+class DecodeCache:
+    """`n_seqs` sequences of one layer, up to `capacity` rows per head.
+
+    rope: Rope or None; q_weight / k_weight: [head_dim] norm weights or None.
+    Keys are rotated (and normed) once, when they arrive; evicted positions
+    leave holes that nothing refers to again, so a kept row is stored as it was.
+    Evicting re-quantises the kept rows in their new blocks.  With cfg.block > 1 an
+    event needs a row count that is a multiple of the block.
+    """
+
+    def __init__(self, cfg: NexusConfig, n_seqs, capacity, budget, walk_iters, *, fmt="e4m3", page_blocks=4,
+                 rope=None, q_weight=None, k_weight=None, eps=1e-6, seed=0, layer=0, head_cap=0, device="cuda"):
+        if cfg.compact:
+            raise ValueError("the kept rows are copied into new blocks: compact must be 0")
+        self.cfg, self.n_seqs, self.capacity = cfg, n_seqs, capacity
+        self.budget, self.walk_iters, self.seed, self.layer = budget, walk_iters, seed, layer
+        self.rope, self.q_weight, self.k_weight, self.eps = rope, q_weight, k_weight, eps
+        hk, d, page = cfg.n_kv_heads, cfg.head_dim, page_blocks * NX_CACHE_BLOCK
+        pages = -(-capacity // page)
+        self.cache = new_paged_cache(cfg, n_seqs, n_seqs * hk * pages, pages, fmt=fmt, page_blocks=page_blocks,
+                                     device=device)
+        self.device = self.cache.device
+        self.cache.table.copy_(torch.arange(n_seqs * hk * pages, dtype=torch.int32).view(n_seqs, hk, pages))
+        self.ws = new_paged_workspace(cfg, self.cache, capacity)
+        self.out = torch.empty(n_seqs, cfg.n_q_heads, d, dtype=cfg.dtype, device=self.device)
+        # The last W rotated queries of every sequence, a ring over dimension 2.
+        self.ring = torch.zeros(n_seqs, cfg.n_q_heads, cfg.window, d, dtype=cfg.dtype, device=self.device)
+        self.queries = 0      # queries seen since load()
+        self.rows = 0         # the host's bound on the heads' row counts
+        self.step_no = 0      # eviction events
+        # An event's buffers: all rows, and the kept ones as [heads][seqs * cap][D].
+        cap = head_cap if head_cap and cfg.head_alloc != NX_HEADS_UNIFORM else budget
+        self.cap_rows = min(cap * cfg.block, capacity)
+        self.k = torch.zeros(n_seqs, hk, capacity, d, dtype=cfg.dtype, device=self.device)
+        self.v = torch.zeros_like(self.k)
+        self.kept_k = torch.zeros(hk, n_seqs * self.cap_rows, d, dtype=cfg.dtype, device=self.device)
+        self.kept_v = torch.zeros_like(self.kept_k)
+        self.keep = torch.zeros(n_seqs, hk, cap, dtype=torch.int32, device=self.device)
+        self.head_budget = torch.zeros(n_seqs, hk, dtype=torch.int32, device=self.device)
+        self.counts = torch.zeros(n_seqs, hk, dtype=torch.int32, device=self.device)
+        self.window = torch.zeros_like(self.ring)
+        self.evict_ws = new_workspace(cfg, capacity, n_seqs, walk_iters, device=self.device)
+        self.head_cap = cap
+        self._units = {}
+
+    def load(self, k, v):
+        """Replaces the rows: k, v [n_seqs, n_kv_heads, rows, D], keys already rotated (a prompt's
+        rows, or the out_k / out_v of a first event)."""
+        n, hk, rows, d = k.shape
+        if rows > self.capacity:
+            raise ValueError(f"{rows} rows, capacity {self.capacity}")
+        self.cache.lens.zero_()
+        if rows:
+            flat = [x.permute(0, 2, 1, 3).reshape(n * rows, hk, d) for x in (k, v)]
+            nx_paged_append(self.cfg, self.cache, *flat, workspace=self.ws)
+        self.rows, self.queries = rows, 0
+
+    def step(self, q, k, v, positions=None):
+        """One new token per sequence: q [n_seqs, n_q_heads, D], k, v [n_seqs, n_kv_heads, D] as
+        projected, positions int32 [n_seqs].  Returns out [n_seqs, n_q_heads, D], which the next
+        step overwrites."""
+        if self.rows + 1 > self.capacity:
+            raise ValueError("the cache is full: evict first")
+        cfg = self.cfg
+        q_rot = self.ring[:, :, self.queries % cfg.window]
+        normed = self.k_weight is not None
+        _, k_new = nx_qk_norm_rope(cfg, q, k if normed else None, workspace=self.ws, q_weight=self.q_weight,
+                                   k_weight=self.k_weight, eps=self.eps, rope=self.rope, positions=positions,
+                                   out_q=q_rot)
+        if normed:       # normed keys come rotated; others are rotated on their way into the cache
+            nx_paged_append(cfg, self.cache, k_new, v, workspace=self.ws)
+        else:
+            nx_paged_append(cfg, self.cache, k, v, workspace=self.ws, rope=self.rope, positions=positions)
+        self.queries += 1
+        self.rows += 1
+        return nx_paged_attn(cfg, self.cache, q_rot, workspace=self.ws, max_tokens=self.rows, out=self.out)
+
+    def evict(self):
+        """One eviction event over all sequences, back to the budget."""
+        cfg, w = self.cfg, self.cfg.window
+        if self.queries < w:
+            raise ValueError(f"an event needs {w} queries, {self.queries} were seen")
+        if self.rows % cfg.block:     # a short last block would be counted as a whole one
+            raise ValueError(f"{self.rows} rows are not whole blocks of {cfg.block}")
+        first = self.queries % w                 # the oldest query's place in the ring
+        self.window[:, :, :w - first].copy_(self.ring[:, :, first:])
+        self.window[:, :, w - first:].copy_(self.ring[:, :, :first])
+        nx_paged_gather(cfg, self.cache, workspace=self.ws, max_tokens=self.rows, out_k=self.k, out_v=self.v)
+        kept = min(cfg.kept_rows(self.rows, self.head_cap), self.cap_rows)
+        units = self._units.get(self.rows)
+        if units is None:
+            d, r = cfg.head_dim, self.cap_rows
+            units = self._units[self.rows] = make_units(
+                [dict(q=self.window[s], k=self.k[s], v=self.v[s], keep=self.keep[s],
+                      out_k=self.kept_k[0, s * r:], out_v=self.kept_v[0, s * r:],
+                      kv_head_stride=self.capacity * d, out_head_stride=self.n_seqs * r * d,
+                      n_tokens=self.rows, budget=self.budget, layer=self.layer, seq_id=s,
+                      head_cap=self.head_cap, head_budget=self.head_budget[s],
+                      head_tokens=self.cache.lens[s], head_tokens_out=self.counts[s])
+                 for s in range(self.n_seqs)], device=self.device)
+        nx_evict_batch(cfg, units, self.n_seqs, self.rows, self.walk_iters, self.seed, workspace=self.evict_ws,
+                       step=self.step_no, max_out_rows=kept)
+        self.cache.lens.zero_()
+        nx_paged_append(cfg, self.cache, self.kept_k.permute(1, 0, 2), self.kept_v.permute(1, 0, 2),
+                        workspace=self.ws, max_new=self.cap_rows, head_new=self.counts)
+        self.rows = kept
+        self.step_no += 1
+
+    def check(self):
+        """Synchronises and raises NexusError on an error that a step or an event recorded."""
+        nx_read_device_status(self.cfg, self.ws)
+        nx_read_device_status(self.cfg, self.evict_ws)

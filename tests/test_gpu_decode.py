@@ -1,0 +1,116 @@
+"""DecodeCache: prompt rows, decode steps, eviction events and decoding on, every stage against the
+oracle or the single calls it is made of."""
+
+import numpy as np
+import pytest
+import torch
+
+import streaming_weighted_sampling_amd as nx
+from oracle import paged
+from tests.test_gpu_paged import DT, Cache, _check_attn, _np, _randn
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+class View(Cache):
+    """The array readers of Cache on a DecodeCache's cache."""
+
+    def __init__(self, d, dtype, fmt):
+        self.cfg, self.c, self.d, self.hkv = d.cfg, d.cache, d.cfg.head_dim, d.cfg.n_kv_heads
+        self.n_seqs, self.group = d.n_seqs, d.cfg.n_q_heads // d.cfg.n_kv_heads
+        self.fmt, self.dtype, self.pb = fmt, dtype, d.cache.k_codes.shape[1]
+
+
+@pytest.mark.parametrize("dtype,fmt,d,normed,alloc,block", [
+    ("bf16", "e4m3", 128, True, 0, 1), ("bf16", "int8", 64, False, 0, 1), ("f32", "int8", 64, False, 2, 1),
+    ("bf16", "e4m3", 64, True, 2, 1), ("bf16", "e4m3", 128, False, 0, 32)])
+def test_decode_evict_decode(dtype, fmt, d, normed, alloc, block):
+    S, hk, grp, W = 2, 2, 4, 8
+    budget = 90 if block == 1 else 3
+    cfg = nx.NexusConfig(hk * grp, hk, d, W, DT[dtype], head_alloc=alloc, head_floor=20 if alloc else 0, block=block)
+    rope = nx.Rope(nx.rope_table(400, d // 2, device=DEV), pairs=True)
+    wq = _randn(1, d, dtype=dtype) if normed else None
+    wk = _randn(2, d, dtype=dtype) if normed else None
+    dec = nx.DecodeCache(cfg, S, 256, budget, 3, fmt=fmt, page_blocks=2, rope=rope, q_weight=wq, k_weight=wk,
+                         seed=7, layer=3, head_cap=150 if alloc else 0, device=DEV)
+    view = View(dec, dtype, fmt)
+    k0, v0 = _randn(3, S, hk, 140, d, dtype=dtype), _randn(4, S, hk, 140, d, dtype=dtype)
+    with pytest.raises(ValueError, match="queries"):
+        dec.evict()
+    dec.load(k0, v0)
+    ws = nx.new_workspace(cfg, 1, 1, 0, device=DEV)
+    pos, seen = 140, []
+
+    def steps(n):
+        nonlocal pos
+        for i in range(n):
+            qkv = _randn(1000 + pos, S, (grp + 2) * hk, d, dtype=dtype)
+            q, k, v = qkv.split((hk * grp, hk, hk), 1)
+            p = torch.full((S,), pos, dtype=torch.int32, device=DEV)
+            out = dec.step(q, k, v, p)
+            want, _ = nx.nx_qk_norm_rope(cfg, q, workspace=ws, q_weight=wq, rope=rope, positions=p)
+            seen.append(want)
+            pos += 1
+            if i % 7 == 0:
+                _check_attn(view, want, [1] * S, out)
+        dec.check()
+
+    steps(20)
+    if block == 1:
+        steps(1)
+    assert dec.cache.lens.flatten().tolist() == [160 + (block == 1)] * (S * hk)
+    for event in range(2):
+        lens = dec.cache.lens.cpu().numpy()
+        gk, gv = nx.nx_paged_gather(cfg, dec.cache, workspace=dec.ws, max_tokens=dec.rows)
+        dec.evict()
+        dec.check()
+        assert torch.equal(dec.window, torch.stack(seen[-W:], 2))
+        counts = dec.counts.cpu().numpy()
+        for s in range(S):
+            for h in range(hk):
+                keep = dec.keep[s, h].cpu().numpy()
+                if block > 1:
+                    keep = np.concatenate([np.arange(b * block, min((b + 1) * block, lens[s, h]))
+                                           for b in keep[:-(-counts[s, h] // block)]])
+                keep = keep[:counts[s, h]]
+                ref = paged.Head(d, dtype, fmt)
+                ref.append(_np(gk[s, h])[keep], _np(gv[s, h])[keep])
+                assert int(dec.cache.lens[s, h]) == len(ref) == counts[s, h]
+                for b, want in enumerate(ref.blocks):
+                    for (codes, scale), (wc, wsc) in zip(view.block(s, h, b), want):
+                        assert scale == wsc and np.array_equal(codes, wc), (s, h, b)
+                for got, want in zip(view.tail(s, h, len(ref) % 32), ref.tail):
+                    assert not want or np.array_equal(got, np.stack(want))
+            if not alloc and event == 0:
+                # the same event by nx_evict_step on the gathered rows
+                n = int(lens[s, 0])
+                ews = nx.new_workspace(cfg, n, 1, 3, device=DEV)
+                keep, _, _ = nx.nx_evict_step(cfg, dec.window[s], gk[s, :, :n].contiguous(),
+                                              gv[s, :, :n].contiguous(), n, budget, 3, 7, workspace=ews, layer=3,
+                                              step=0, seq_id=s)
+                assert torch.equal(keep, dec.keep[s])
+        if alloc:
+            assert counts.sum() == S * hk * budget and len(set(counts.flatten())) > 1
+        steps(40)
+        if block > 1:
+            with pytest.raises(ValueError, match="whole blocks"):
+                dec.evict()
+            steps(24)
+
+
+def test_decode_cache_refuses_what_it_cannot_hold():
+    cfg = nx.NexusConfig(4, 2, 64, 4)
+    with pytest.raises(ValueError, match="compact"):
+        nx.DecodeCache(nx.NexusConfig(4, 2, 64, 4, compact=1), 1, 64, 32, 1, device=DEV)
+    dec = nx.DecodeCache(cfg, 1, 64, 32, 1, page_blocks=1, device=DEV)
+    with pytest.raises(ValueError, match="capacity"):
+        dec.load(*[torch.zeros(1, 2, 65, 64, dtype=torch.bfloat16, device=DEV)] * 2)
+    dec.load(*[torch.zeros(1, 2, 64, 64, dtype=torch.bfloat16, device=DEV)] * 2)
+    q, k = _randn(1, 1, 4, 64, dtype="bf16"), _randn(2, 1, 2, 64, dtype="bf16")
+    with pytest.raises(ValueError, match="full"):
+        dec.step(q, k, k)
+    dec.load(*[torch.zeros(1, 2, 0, 64, dtype=torch.bfloat16, device=DEV)] * 2)
+    out = dec.step(q, k, k)              # the first row of an empty cache: attention is that row
+    dec.check()
+    assert torch.equal(out, k.repeat_interleave(2, 1))
