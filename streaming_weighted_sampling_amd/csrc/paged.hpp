@@ -24,11 +24,15 @@ struct PagedArgs {
   int32_t page_shift;      // log2(page_blocks)
   uint32_t* status;
   // attention
-  int32_t group, max_q, n_rt, n_splits, chunk;   // row tiles, splits, blocks per chunk
+  int32_t group, max_q, n_rt, n_wg;   // query-row tiles, shares
+  int32_t min_share;       // fewest blocks of a share
+  int32_t whole;           // 1: a workgroup per head, no shares
+  int32_t stream_nt;       // 1: the codes are read past the caches
   float scale_log2;        // scale * log2(e)
   float* lse;
-  float* part_o;           // [units * n_rt * n_splits][tile rows][D]
-  float* part_ml;          // [units * n_rt * n_splits][tile rows][2]: (max, sum), log2 units
+  int2* pieces;            // [units]: a head's pieces (0: written whole) and its first partial
+  float* part_o;           // [2 * n_wg][n_rt][tile rows][D]
+  float* part_ml;          // [2 * n_wg][n_rt][tile rows][2]: (base, sum), log2 units
   // gather
   int32_t max_tokens;
   void* out_k;
@@ -52,9 +56,9 @@ hipError_t launch_paged_attn(const PagedArgs& a, hipStream_t s);
 hipError_t launch_paged_gather(const PagedArgs& a, hipStream_t s);
 hipError_t launch_norm_rope(const NormArgs& a, hipStream_t s);
 
-// Query rows per tile and workgroup (a multiple of 16) of a call with `rows`
-// = queries * group rows per (sequence, KV head).
-int paged_tile_rows(int64_t rows, int dtype);
+// Query rows per tile of a call with `rows` = queries * group rows per
+// (sequence, KV head).
+int paged_tile_rows(int64_t rows);
 
 // ---- device side ----
 
@@ -66,14 +70,17 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 template <bool kF32> struct Elem;
 template <> struct Elem<false> {
   static constexpr int kBytes = 2;
-  static __device__ void load8(const void* p, float (&x)[8]) {
-    const uint4 w = *static_cast<const uint4*>(p);
+  // 8 elements from one 16-byte word (fp32: two).
+  static __device__ void unpack8(uint4 w, uint4, float (&x)[8]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = __builtin_bit_cast(float, u[i] << 16);
       x[2 * i + 1] = __builtin_bit_cast(float, u[i] & 0xFFFF0000u);
     }
+  }
+  static __device__ void load8(const void* p, float (&x)[8]) {
+    unpack8(*static_cast<const uint4*>(p), uint4{}, x);
   }
   static __device__ float round(float x) { return float(__bf16(x)); }
   static __device__ uint32_t pack2(float a, float b) {
@@ -96,10 +103,13 @@ template <> struct Elem<false> {
 };
 template <> struct Elem<true> {
   static constexpr int kBytes = 4;
-  static __device__ void load8(const void* p, float (&x)[8]) {
-    const float4 a = static_cast<const float4*>(p)[0], b = static_cast<const float4*>(p)[1];
+  static __device__ void unpack8(uint4 v, uint4 w, float (&x)[8]) {
+    const float4 a = __builtin_bit_cast(float4, v), b = __builtin_bit_cast(float4, w);
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+  static __device__ void load8(const void* p, float (&x)[8]) {
+    unpack8(static_cast<const uint4*>(p)[0], static_cast<const uint4*>(p)[1], x);
   }
   static __device__ float round(float x) { return x; }
   static __device__ void store8(void* p, const float (&x)[8]) {

@@ -11,10 +11,15 @@ using namespace nx;
 namespace {
 
 constexpr int64_t kMaxCacheRows = int64_t(1) << 24;
-constexpr int kMaxChunk = 256;     // blocks per chunk: 64 per wavefront, one lane each
-// Workgroups an attention call is split into: 8 per CU keep every CU's loads in
-// flight and leave the uneven heads of a ragged batch to the hardware's balance.
-constexpr int kTargetGroups = 2048;
+constexpr int64_t kCUs = 256;
+// Resident attention workgroups per CU (registers): 16-row and 32-row tiles.
+constexpr int64_t kResident16 = 1, kResident32 = 2;
+constexpr int64_t kMinShare = 4;        // blocks: one per wavefront
+// Heads of up to this many rows are taken whole by a workgroup each (8 heads of
+// 1024 rows: 9.5 us, in shares 9.3; of 819: 9.2 and 12.3), of up to twice as many
+// where there are kManyHeads of them (128 of 2048: 15.8 and 19.3).
+constexpr int64_t kWholeTokens = 1024, kManyHeads = 64;
+constexpr int64_t kStreamBytes = int64_t(256) << 20;
 
 int32_t elem_size(int32_t dtype) { return dtype == NX_BF16 ? 2 : 4; }
 bool aligned(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -123,31 +128,33 @@ PagedArgs base_args(const nx_paged* c) {
   return a;
 }
 
-// How an attention call is cut: query-row tiles, chunks of blocks, splits.
+// How an attention call is cut: query-row tiles and shares of the line of blocks.
 struct Cut {
-  int32_t tile, n_rt, chunk, n_splits;
-  int64_t slots;         // bound on units * n_rt * n_splits for any smaller max_tokens too
+  int64_t tile, n_rt, n_wg;
+  int64_t bytes;         // of codes, at max_tokens rows a head
+  bool whole;            // a workgroup per head and row tile
 };
 nx_status make_cut(const nx_paged* c, int64_t max_tokens, int64_t max_q, Cut* out) {
   if (max_tokens < 0 || max_q < 1) return NX_EINVAL;
   const int64_t rows = max_q * (c->n_q_heads / c->n_kv_heads);
   if (max_tokens > kMaxCacheRows || rows > (int64_t(1) << 20)) return NX_EUNSUPPORTED;
-  const int64_t tile = paged_tile_rows(rows, c->dtype);
+  const int64_t tile = paged_tile_rows(rows);
   const int64_t n_rt = (rows + tile - 1) / tile;
-  const int64_t work = int64_t(c->n_seqs) * c->n_kv_heads * n_rt;
-  const int64_t blocks = std::max<int64_t>(1, (max_tokens + kBlock - 1) / kBlock);
-  // Equal chunks, a multiple of the four wavefronts' blocks.
-  int64_t chunk = ((work * blocks + kTargetGroups - 1) / kTargetGroups + 3) / 4 * 4;
-  chunk = std::min<int64_t>(chunk, kMaxChunk);
-  const int64_t most = std::max<int64_t>(1, kTargetGroups / work);
-  *out = {int32_t(tile), int32_t(n_rt), int32_t(chunk),
-          int32_t(std::min((blocks + chunk - 1) / chunk, most + 1)),
-          std::min(kTargetGroups + work, work * ((blocks + 3) / 4))};
+  const int64_t units = int64_t(c->n_seqs) * c->n_kv_heads;
+  // One round of workgroups fills the chip (kResident per CU); no more than
+  // there are smallest shares.
+  const int64_t blocks = units * std::max<int64_t>(1, (max_tokens + kBlock - 1) / kBlock);
+  const int64_t most = std::max<int64_t>(8, kCUs * (tile == 16 ? kResident16 : kResident32) / n_rt);
+  const int64_t n_wg = std::min(most, (blocks + kMinShare - 1) / kMinShare);
+  *out = {tile, n_rt, (n_wg + 7) / 8 * 8, blocks * kBlock * 2 * c->head_dim,
+          max_tokens <= (units >= kManyHeads ? 2 * kWholeTokens : kWholeTokens)};
   return NX_OK;
 }
-size_t part_ml_bytes(const Cut& k) { return align256(size_t(k.slots) * k.tile * 2 * sizeof(float)); }
+// Workspace: status word, the heads' pieces, partials.
+size_t pieces_bytes(const nx_paged* c) { return align256(size_t(c->n_seqs) * c->n_kv_heads * sizeof(int2)); }
+size_t part_ml_bytes(const Cut& k) { return align256(size_t(2 * k.n_wg * k.n_rt * k.tile) * 2 * sizeof(float)); }
 size_t cut_bytes(const nx_paged* c, const Cut& k) {
-  return 256 + part_ml_bytes(k) + size_t(k.slots) * k.tile * c->head_dim * sizeof(float);
+  return 256 + pieces_bytes(c) + part_ml_bytes(k) + size_t(2 * k.n_wg * k.n_rt * k.tile) * c->head_dim * sizeof(float);
 }
 
 }  // namespace
@@ -272,12 +279,16 @@ nx_status nx_paged_attn(const nx_paged* cache, const nx_rows* q, const nx_rows* 
   a.n_rows = n_rows;
   a.start = q_start;
   a.max_q = max_q;
-  a.n_rt = cut.n_rt;
-  a.n_splits = cut.n_splits;
-  a.chunk = cut.chunk;
+  a.n_rt = int32_t(cut.n_rt);
+  a.n_wg = int32_t(cut.n_wg);
+  a.min_share = int32_t(kMinShare);
+  a.whole = cut.whole;
+  a.stream_nt = cut.n_rt == 1 && cut.bytes > kStreamBytes;
   a.scale_log2 = float((scale > 0.f ? double(scale) : 1.0 / std::sqrt(double(d))) * 1.4426950408889634);
   a.lse = out_lse;
   char* ws = static_cast<char*>(cache->workspace) + 256;
+  a.pieces = reinterpret_cast<int2*>(ws);
+  ws += pieces_bytes(cache);
   a.part_ml = reinterpret_cast<float*>(ws);
   a.part_o = reinterpret_cast<float*>(ws + part_ml_bytes(cut));
   hipStream_t s = static_cast<hipStream_t>(cache->stream);

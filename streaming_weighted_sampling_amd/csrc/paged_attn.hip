@@ -3,10 +3,13 @@
 //   o_r = sum_t p_rt v_t / sum_t p_rt,   p_rt = exp(scale q_r . k_t - m_r)
 //
 // One pass over the cached rows with a running reference m_r and sum per query
-// row.  Work is split over (sequence, KV head) x query-row tile x chunk of
-// blocks; four wavefronts of a workgroup take the blocks of a chunk, merge
-// through LDS, and write either the result or a partial (m, sum, o) that
-// attn_combine merges.
+// row.  The blocks of all (sequence, KV head)s form one line that is cut into
+// equal shares, one per workgroup, whatever the heads' lengths: every CU gets
+// the same bytes, in one round.  A share covers pieces of one or several
+// heads; the four wavefronts split a piece and merge through LDS.  A head that
+// lies in one share is written at once, otherwise its pieces leave partials
+// (m, sum, o) and the last workgroup to arrive merges them in head order, so
+// the result does not depend on the order of arrival.
 //
 // Matrix form, per block of 32 rows: S^T = K Q^T and O^T += V^T P^T with
 // 16x16x32 f16 MFMAs.  8-bit codes are exact in f16, so the codes are the
@@ -27,12 +30,16 @@
 namespace nx {
 namespace {
 
-constexpr float kNoMax = -1e30f;   // reference of a row that has seen nothing
-// p is held times 2^7 and may exceed its reference by 2^7, V's scale ratio is at
-// most 2: f16 values stay below 2^15.
+constexpr float kNoBase = 1e30f;     // base of a row that has seen nothing
+constexpr float kNoScale = -200.f;   // log2 of V's reference before the first block
+// p is held times 2^7 at its row's reference and may grow by 2^7 (times V's
+// scale ratio, at most 2) before the reference moves: f16 values stay below 2^15.
 constexpr float kHead = 7.f;
-// Smallest V scale ratio that multiplies p: p keeps 11 bits down to 2^-9 there.
-constexpr float kApart = 0x1p-12f;
+// V's scale ratio is taken as at least 2^-40: times p, at most 2^14, that is
+// below half of f16's smallest step, so such a block adds nothing to o.  In
+// general o is exact to 2^-31 of the head's largest |v| for each row, from
+// f16's smallest step.  (The tail's p is not held in f16.)
+constexpr float kLeast = -40.f, kLeastTail = -80.f;
 
 template <int kFmt>
 __device__ inline h8_t codes_f16(uint32_t lo, uint32_t hi) {
@@ -55,309 +62,437 @@ __device__ inline h8_t codes_f16(uint32_t lo, uint32_t hi) {
   return r.v;
 }
 
-// What a workgroup works on.
+// One (sequence, KV head) as the kernel sees it.
 struct Job {
-  int unit, rt, split;
   int n_q, rows;       // queries of the sequence, query rows (queries * group)
   int64_t q0;          // first row in q / out
-  int len, n_blk;      // cached rows; blocks, the tail counted as one
+  int len, n_blk;      // cached rows; its weight in the line of blocks: blocks
+                       // (the tail counts as one), at least 1; 0 without queries
   bool ok;
 };
-__device__ inline Job make_job(const PagedArgs& a, int unit, int rt, int split) {
+__device__ inline Job make_job(const PagedArgs& a, int unit) {
   Job j;
-  j.unit = unit;
-  j.rt = rt;
-  j.split = split;
-  const int s = unit / a.c.n_kv_heads;
-  j.n_q = seq_rows(a, s, a.max_q, &j.q0);
+  j.n_q = seq_rows(a, unit / a.c.n_kv_heads, a.max_q, &j.q0);
   j.len = a.c.lens[unit];
   j.ok = j.n_q >= 0 && j.len >= 0 &&
          int64_t(j.len) <= (int64_t(a.c.max_pages) << a.page_shift) * kBlock;
   j.rows = j.ok ? j.n_q * a.group : 0;
   if (!j.ok) j.len = 0;
-  j.n_blk = (j.len + kBlock - 1) / kBlock;
+  j.n_blk = j.rows > 0 ? max(1, (j.len + kBlock - 1) / kBlock) : 0;
   return j;
 }
 
-template <int D, int RT>
-struct State {
-  f32x4_t o[RT][D / 16];
-  float m[RT], l[RT];
-  float vref;
+// Sum over the lanes below and including this one (row shifts within 16 lanes,
+// then row broadcasts: VALU only).
+__device__ inline int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);   // row_shr:1
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);   // row_shr:2
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);   // row_shr:4
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);   // row_shr:8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);   // row_bcast:15 to rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);   // row_bcast:31 to rows 2 and 3
+  return x;
+}
+
+// This workgroup's share [begin, end) of the line and the head it starts in.
+struct Share {
+  int size, begin, end;
+  int unit;            // first head with blocks in the share
+  int unit_at;         // where that head starts in the line
 };
 
-// Folds the logits z[rt][0..7] (log2 units, already minus m - kHead) of one
-// block into the state: p = 2^z, scaled by vs / vref for the V product.
-// `y(rt, e)` recomputes a masked logit when a reference has to move.
-template <int D, int RT, typename Y>
-__device__ inline void settle(State<D, RT>& st, float (&z)[RT][8], float vs, float& ratio, Y&& y) {
-  float top = z[0][0];
+// Every wavefront sums the heads' weights for itself, 64 heads at a time: no
+// barrier, and the sums of all workgroups are the same.
+__device__ inline Share find_share(const PagedArgs& a, int wg, int units, int lane) {
+  auto weight = [&](int unit) {
+    if (unit >= units) return 0;
+    const Job j = make_job(a, unit);
+    if (!j.ok && wg == 0) paged_status(a.status, kStatusBadItem);
+    return j.n_blk;
+  };
+  Share s;
+  int64_t total = 0;
+  int mine = 0, incl = 0;
+  for (int u0 = 0; u0 < units; u0 += 64) {
+    mine = weight(u0 + lane);
+    incl = wave_scan(mine);
+    total += __builtin_amdgcn_readlane(incl, 63);
+  }
+  if (total > INT32_MAX) {   // more blocks than a pool can hold many times over
+    if (wg == 0) paged_status(a.status, kStatusBadItem);
+    total = 0;
+  }
+  s.size = max(a.min_share, int((uint32_t(total) + uint32_t(a.n_wg) - 1) / uint32_t(a.n_wg)));
+  const int64_t begin = int64_t(wg) * s.size;
+  s.begin = int(min(begin, total));
+  s.end = int(min(begin + s.size, total));
+  s.unit = s.unit_at = 0;
+  for (int u0 = 0, at = 0; s.begin < s.end && u0 < units; u0 += 64) {
+    if (units > 64) {
+      mine = weight(u0 + lane);
+      incl = wave_scan(mine);
+    }
+    const uint64_t hit = __ballot(mine > 0 && at + incl - mine <= s.begin && s.begin < at + incl);
+    if (hit != 0) {
+      const int i = __builtin_ctzll(hit);
+      s.unit = u0 + i;
+      s.unit_at = at + __builtin_amdgcn_readlane(incl - mine, i);
+      break;
+    }
+    at += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return s;
+}
+
+// Accumulators of a wavefront: query row c of tile rt in lanes (., c).
+template <int D, int RT>
+struct State {
+  f32x4_t o[RT][D / 16];   // in units of vref
+  float base[RT];          // p = 2^(logit + base), logits in log2 units
+  float l[RT];             // sum of p over this lane's tokens
+  float vref, lvref;       // V's reference scale (wave-uniform) and its log2
+};
+
+__device__ inline float uniform(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
+}
+__device__ inline float lane_of(float x, int i) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), i));
+}
+
+// The exponents z of one block's p from its products s (-infinity: hidden),
+// with the block's V scale vs over the reference in them; moves references.
+// t[rt] > 0: factor to log2 units; lvs: log2(vs); the ratio counts as at least
+// 2^least.  Returns the power that the sum of p takes out again (log2 of the
+// ratio is good to 2^-20, the sum sees the same value).
+template <int D, int RT>
+__device__ inline float exponents(State<D, RT>& st, const f32x4_t (&s)[RT][2], const float (&t)[RT], float vs,
+                                  float lvs, float least, float (&z)[RT][8]) {
+  float shift = fmaxf(lvs - st.lvref, least);
+  float top = -__builtin_inff();
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
+  for (int rt = 0; rt < RT; ++rt) {
+    const float b = st.base[rt] + shift;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = fmaxf(top, z[rt][e]);
-  if (__any(top > 2.f * kHead) || vs > 2.f * st.vref) {
+    for (int e = 0; e < 8; ++e) {
+      z[rt][e] = __builtin_fmaf(s[rt][e / 4][e % 4], t[rt], b);
+      top = fmaxf(top, z[rt][e]);
+    }
+  }
+  if (__any(top > 2.f * kHead) || shift > 1.f) {
     // Rare: a row's reference moves to its largest logit so far, or V's
     // reference scale to this block's; what is accumulated follows.
     float f = 1.f;
-    if (vs > 2.f * st.vref) {
-      f = st.vref / vs;
+    if (shift > 1.f) {
+      f = uniform(st.vref / vs);
       st.vref = vs;
+      st.lvref = lvs;
+      shift = 0.f;
     }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      float mx = st.m[rt];
+      float mx = kHead - st.base[rt];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) mx = fmaxf(mx, y(rt, e));
+      for (int e = 0; e < 8; ++e) mx = fmaxf(mx, s[rt][e / 4][e % 4] * t[rt]);
       mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
       mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-      const float alpha = exp2f(st.m[rt] - mx);
-      st.m[rt] = mx;
+      const float base = kHead - mx;
+      const float alpha = __builtin_amdgcn_exp2f(base - st.base[rt]);
+      st.base[rt] = base;
       st.l[rt] *= alpha;
 #pragma unroll
       for (int n = 0; n < D / 16; ++n) st.o[rt][n] *= alpha * f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[rt][e] = y(rt, e) - (mx - kHead);
+      for (int e = 0; e < 8; ++e)
+        z[rt][e] = __builtin_fmaf(s[rt][e / 4][e % 4], t[rt], base + shift);
     }
   }
-  ratio = st.vref > 0x1p-120f ? vs / st.vref : 0.f;
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      z[rt][e] = __builtin_amdgcn_exp2f(z[rt][e]);
-      st.l[rt] += z[rt][e];
-    }
+  return __builtin_amdgcn_exp2f(-shift);
 }
 
-template <int D, bool kF32, int kFmt, int RT>
-__global__ __launch_bounds__(256) void attn_kernel(PagedArgs a) {
+// z becomes p, the sums take it up.
+template <int D, int RT>
+__device__ inline void exponentiate(State<D, RT>& st, float back, float (&z)[RT][8]) {
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[rt][e] = __builtin_amdgcn_exp2f(z[rt][e]);
+    const float sum = ((z[rt][0] + z[rt][1]) + (z[rt][2] + z[rt][3])) +
+                      ((z[rt][4] + z[rt][5]) + (z[rt][6] + z[rt][7]));
+    st.l[rt] = __builtin_fmaf(sum, back, st.l[rt]);
+  }
+}
+
+// The query rows of one tile: where row (rt, c) lies, or null past the last.
+template <bool kF32>
+__device__ inline int64_t row_offset(const PagedArgs& a, const nx_rows& rows, const Job& job, int h, int r) {
+  const int i = r / a.group, gh = r - i * a.group;
+  return ((job.q0 + i) * rows.row_stride + (int64_t(h) * a.group + gh) * rows.head_stride) *
+         Elem<kF32>::kBytes;
+}
+
+__device__ inline void write_lse(const PagedArgs& a, const Job& job, int h, int r, float l, float base) {
+  const int i = r / a.group, gh = r - i * a.group;
+  a.lse[(job.q0 + i) * a.c.n_q_heads + h * a.group + gh] =
+      l == 0.f ? -__builtin_inff() : 0.69314718056f * (log2f(l) - base);
+}
+
+// Partial of share `wg` for the head that starts at unit_at: a share holds at
+// most two, one for a head that covers its start and one for a head that
+// begins inside it and goes on past its end.
+__device__ inline int64_t part_slot(const Share& share, int unit_at, int wg) {
+  return 2 * int64_t(wg) + (unit_at > int64_t(wg) * share.size ? 1 : 0);
+}
+
+// 16 RT query rows a workgroup.  kWhole: workgroup (u, row tile) takes head u
+// whole, for calls of short heads, which then need neither the search for the
+// share nor the merge launch.
+template <int D, bool kF32, int kFmt, int RT, bool kNT, bool kWhole, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void attn_kernel(PagedArgs a) {
   using E = Elem<kF32>;
   constexpr int kC = D / 32;          // 32-element chunks of a row
   constexpr int NP = kF32 ? 2 : 1;    // f16 terms of q and p
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int c16 = lane & 15, g = lane >> 4;
-  const int split = blockIdx.x % a.n_splits, rt0 = blockIdx.x / a.n_splits;
-  const Job job = make_job(a, blockIdx.y, rt0, split);
-  if (!job.ok) {
-    if (blockIdx.x == 0 && tid == 0) paged_status(a.status, kStatusBadItem);
-    return;
-  }
-  const int row0 = rt0 * RT * 16;
-  if (row0 >= job.rows) return;
-  if (split > 0 && split * a.chunk >= job.n_blk) return;
-  const int h = job.unit % a.c.n_kv_heads;
-
-  // ---- q: f16 operand terms and the factor of the logits per row ----
-  h8_t q[RT][kC][NP];
-  float qmul[RT];
-  auto q_row = [&](int rt) -> const char* {
-    const int r = row0 + rt * 16 + c16;
-    if (r >= job.rows) return nullptr;
-    const int i = r / a.group, gh = r - i * a.group;
-    return static_cast<const char*>(a.q.p) +
-           ((job.q0 + i) * a.q.row_stride + (int64_t(h) * a.group + gh) * a.q.head_stride) * E::kBytes;
-  };
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const char* p = q_row(rt);
-    float x[kC][8];
-    float top = 0.f;
-#pragma unroll
-    for (int c = 0; c < kC; ++c) {
-      if (p != nullptr) {
-        E::load8(p + (64 * (c / 2) + 16 * g + 8 * (c % 2)) * E::kBytes, x[c]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[c][e] = 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[c][e]));
-    }
-    top = fmaxf(top, __shfl_xor(top, 16, 64));
-    top = fmaxf(top, __shfl_xor(top, 32, 64));
-    const int ex = top > 0.f ? int(__builtin_bit_cast(uint32_t, top) >> 23) - 127 : 0;
-#pragma unroll
-    for (int c = 0; c < kC; ++c)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float s = ldexpf(x[c][e], 13 - ex);
-        const _Float16 hi = _Float16(s);
-        q[rt][c][0][e] = hi;
-        if constexpr (kF32) q[rt][c][NP - 1][e] = _Float16(s - float(hi));
-      }
-    qmul[rt] = ldexpf(a.scale_log2, ex - 13);
-  }
-
-  State<D, RT> st;
-  st.vref = 0.f;
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    st.m[rt] = kNoMax;
-    st.l[rt] = 0.f;
-#pragma unroll
-    for (int n = 0; n < D / 16; ++n) st.o[rt][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  }
-  // Row r sees tokens up to seen[rt]; tokens from first_hidden on need the test.
-  int seen[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-    seen[rt] = job.len - job.n_q + (row0 + rt * 16 + c16) / a.group;
-  const int all_see = job.len - job.n_q;
-
-  const int full = job.len / kBlock;
+  constexpr int kRows = RT * 16;
+  constexpr int kKL = D / 64 * 2, kVL = D / 32;   // 16-byte loads of a block
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int units = a.c.n_seqs * a.c.n_kv_heads;
   const int slot_mask = (1 << a.page_shift) - 1;
-  const int64_t trow = int64_t(job.unit) * a.c.max_pages;
-  for (int c0 = split * a.chunk; c0 < job.n_blk; c0 += a.n_splits * a.chunk) {
-    const int c1 = min(c0 + a.chunk, job.n_blk);
-    const int per = (c1 - c0 + 3) / 4;
-    const int w0 = c0 + wave * per, w1 = min(w0 + per, c1);
-    const int n8 = min(w1, full) - w0;   // whole blocks of this wavefront, at most 64
-    // Lane j looks up block w0 + j.
-    int slot_l = 0;
-    float ks_l = 0.f, vs_l = 0.f;
-    if (lane < n8) {
-      const int b = w0 + lane;
-      int page = a.c.table[trow + (b >> a.page_shift)];
-      if (page < 0 || page >= a.c.n_pages) {
-        paged_status(a.status, kStatusBadItem);
-        page = 0;
-      }
-      slot_l = (page << a.page_shift) + (b & slot_mask);
-      ks_l = a.c.k_scale[slot_l];
-      vs_l = a.c.v_scale[slot_l];
+  __shared__ float sb[kWaves][kRows], sl[kWaves][kRows];
+  __shared__ f32x4_t so[kWaves][RT * (D / 16)][64];
+
+  // Workgroups of one share and all its row tiles sit on one XCD (ids eight
+  // apart) and near in time, so that the tiles share its L2.
+  const int per8 = 8 * a.n_rt;
+  const int wg = !kWhole ? int(blockIdx.x) / per8 * 8 + int(blockIdx.x) % 8 : 0;
+  const int rt0 = !kWhole ? int(blockIdx.x) % per8 / 8 : int(blockIdx.x) % a.n_rt;
+  const int row0 = rt0 * kRows;
+  Share share;
+  if constexpr (!kWhole) {
+    share = find_share(a, wg, units, threadIdx.x & 63);
+  } else {
+    share.begin = share.unit_at = 0;
+    share.unit = int(blockIdx.x) / a.n_rt;
+    const Job job = make_job(a, share.unit);
+    if (!job.ok && rt0 == 0 && threadIdx.x == 0) paged_status(a.status, kStatusBadItem);
+    share.size = max(1, job.n_blk);
+    share.end = job.n_blk;
+  }
+  int at = share.unit_at;
+  int unit = share.unit;
+  for (int pos = share.begin; pos < share.end; ++unit) {
+    const Job job = make_job(a, unit);
+    const int unit_at = at;
+    at += job.n_blk;
+    const int b0 = pos - unit_at;
+    const int b1 = min(job.n_blk, share.end - unit_at);
+    if (job.n_blk == 0) continue;
+    pos = unit_at + b1;
+    if (row0 >= job.rows) continue;
+    const int h = unit % a.c.n_kv_heads;
+    // The lane is opaque in every piece: what depends on it alone is computed
+    // again (a few instructions) and not kept in registers over the loop.
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int c16 = lane & 15, g = lane >> 4;
+
+    State<D, RT> st;
+    st.vref = 0.f;
+    st.lvref = kNoScale;
+    // Row r sees tokens up to seen[rt]; blocks past all_see need the test.
+    int seen[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      st.base[rt] = kNoBase;
+      st.l[rt] = 0.f;
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) st.o[rt][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      seen[rt] = job.len - job.n_q + (row0 + rt * 16 + c16) / a.group;
     }
-    constexpr int kKL = D / 64 * 2, kVL = D / 32;   // 16-byte loads of a block
+    const int all_see = job.len - job.n_q;
+    const int full = job.len / kBlock;
+    const int per = (b1 - b0 + kWaves - 1) / kWaves;
+    const int w0 = b0 + wave * per, w1 = min(w0 + per, b1), wf = min(w1, full);
+    // Lane j looks up block x0 + j of up to 64 blocks.
+    int slot_l, n8;
+    float ks_l, vs_l;
+    auto look_up = [&](int x0) {
+      n8 = min(wf - x0, 64);
+      slot_l = 0;
+      ks_l = vs_l = 0.f;
+      if (lane < n8) {
+        const int b = x0 + lane;
+        int page = a.c.table[int64_t(unit) * a.c.max_pages + (b >> a.page_shift)];
+        if (page < 0 || page >= a.c.n_pages) {
+          paged_status(a.status, kStatusBadItem);
+          page = 0;
+        }
+        slot_l = (page << a.page_shift) + (b & slot_mask);
+        ks_l = a.c.k_scale[slot_l];
+        vs_l = a.c.v_scale[slot_l];
+      }
+    };
+    // A block's K is fetched while the block before is settled, its V while
+    // its own logits form: each register is refilled as soon as it is used.
     uint4 kr[kKL], vr[kVL];
-    auto load = [&](int i) {
-      const int64_t base = int64_t(__builtin_amdgcn_readlane(slot_l, i)) * kBlock * D;
-      const Buf kb(static_cast<const char*>(a.c.k_codes) + base, kBlock * D);
-      const Buf vb(static_cast<const char*>(a.c.v_codes) + base, kBlock * D);
+    auto codes = [&](const void* base, int i) {
+      const int64_t at = int64_t(__builtin_amdgcn_readlane(slot_l, i)) * (kBlock * D);
+      return Buf(static_cast<const char*>(base) + at, kBlock * D);
+    };
+    auto load_k = [&](int i) {
+      const Buf kb = codes(a.c.k_codes, i);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int x = 0; x < D / 64; ++x)
           kr[u * (D / 64) + x] =
-              kb.ld16(((c16 / 4) * 8 + u * 4 + c16 % 4) * D + 64 * x + 16 * g);
-#pragma unroll
-      for (int n = 0; n < kVL; ++n) vr[n] = vb.ld16((g * D + 32 * n + 2 * c16) * 8);
+              kb.ld16<kNT ? kNonTemporal : 0>(((c16 / 4) * 8 + c16 % 4) * D + 16 * g + u * 4 * D + 64 * x);
     };
-    if (n8 > 0) load(0);
-    for (int i = 0; i < n8; ++i) {
-      uint4 kc[kKL], vc[kVL];
+    auto load_v = [&](int i) {
+      const Buf vb = codes(a.c.v_codes, i);
 #pragma unroll
-      for (int x = 0; x < kKL; ++x) kc[x] = kr[x];
+      for (int n = 0; n < kVL; ++n) vr[n] = vb.ld16<kNT ? kNonTemporal : 0>((g * D + 2 * c16) * 8 + 256 * n);
+    };
+    // The first block is on its way while q is prepared.
+    if (w0 < wf) {
+      look_up(w0);
+      load_k(0);
+      load_v(0);
+    }
+
+    // ---- q: f16 operand terms and the factor of the logits per row ----
+    h8_t q[RT][kC][NP];
+    float qmul[RT];
 #pragma unroll
-      for (int x = 0; x < kVL; ++x) vc[x] = vr[x];
-      if (i + 1 < n8) load(i + 1);
-      const float ks = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ks_l), i));
-      const float vs = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, vs_l), i));
+    for (int rt = 0; rt < RT; ++rt) {
+      const int r = row0 + rt * 16 + c16;
+      const char* src = static_cast<const char*>(a.q.p) + row_offset<kF32>(a, a.q, job, h, min(r, job.rows - 1));
+      float x[kC][8];
+      float top = 0.f;
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        E::load8(src + (64 * (c / 2) + 16 * g + 8 * (c % 2)) * E::kBytes, x[c]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (r >= job.rows) x[c][e] = 0.f;
+          top = fmaxf(top, fabsf(x[c][e]));
+        }
+      }
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      const int ex = top > 0.f ? int(__builtin_bit_cast(uint32_t, top) >> 23) - 127 : 0;
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float s = ldexpf(x[c][e], 13 - ex);
+          const _Float16 hi = _Float16(s);
+          q[rt][c][0][e] = hi;
+          if constexpr (kF32) q[rt][c][NP - 1][e] = _Float16(s - float(hi));
+        }
+      qmul[rt] = ldexpf(a.scale_log2, ex - 13);
+    }
+
+    for (int x0 = w0; x0 < wf; x0 += 64) {
+      if (x0 > w0) {
+        look_up(x0);
+        load_k(0);
+        load_v(0);
+      }
+      const float lvs_l = vs_l > 0.f ? log2f(vs_l) : kNoScale * 4.f;
       f32x4_t s[RT][2];
+      auto products = [&] {   // s = K q^T of the block in kr
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int c = 0; c < kC; ++c) {
-          const uint4 w = kc[u * (D / 64) + c / 2];
-          const h8_t k8 = c % 2 ? codes_f16<kFmt>(w.z, w.w) : codes_f16<kFmt>(w.x, w.y);
+          for (int c = 0; c < kC; ++c) {
+            const uint4 w = kr[u * (D / 64) + c / 2];
+            const h8_t k8 = c % 2 ? codes_f16<kFmt>(w.z, w.w) : codes_f16<kFmt>(w.x, w.y);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+              for (int np = 0; np < NP; ++np)
+                s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, q[rt][c][np], s[rt][u], 0, 0, 0);
+          }
+      };
+      for (int i = 0; i < n8; ++i) {
+        products();
+        if (i + 1 < n8) load_k(i + 1);
+        const float ks = lane_of(ks_l, i), vs = lane_of(vs_l, i), lvs = lane_of(lvs_l, i);
+        float t[RT], z[RT][8];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) t[rt] = fmaxf(ks * qmul[rt], 0x1p-126f);   // > 0: hidden stays -infinity
+        const int t0 = (x0 + i) * kBlock;
+        if (t0 + kBlock - 1 > all_see) {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-            for (int np = 0; np < NP; ++np)
-              s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, q[rt][c][np], s[rt][u], 0, 0, 0);
+            for (int e = 0; e < 8; ++e)
+              if (t0 + 8 * g + e > seen[rt]) s[rt][e / 4][e % 4] = -__builtin_inff();
         }
-      const int t0 = (w0 + i) * kBlock;
-      const bool hide = t0 + kBlock - 1 > all_see;
-      float z[RT][8];
-      auto logit = [&](int rt, int e) {
-        const float y = s[rt][e / 4][e % 4] * (ks * qmul[rt]);
-        return hide && t0 + 8 * g + e > seen[rt] ? -__builtin_inff() : y;
-      };
+        const float back = exponents<D, RT>(st, s, t, vs, lvs, kLeast, z);
+        exponentiate<D, RT>(st, back, z);
+        h8_t pp[RT][NP];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
+        for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) z[rt][e] = logit(rt, e) - (st.m[rt] - kHead);
-      float ratio;
-      settle<D, RT>(st, z, vs, ratio, logit);
-      // A block whose V scale is far below the reference would push p out of
-      // f16's range: its product is formed apart and scaled in fp32.
-      const bool apart = ratio < kApart;
-      const float pscale = apart ? 1.f : ratio;
-      h8_t pp[RT][NP];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x = z[rt][e] * pscale;
-          const _Float16 hi = _Float16(x);
-          pp[rt][0][e] = hi;
-          if constexpr (kF32) pp[rt][NP - 1][e] = _Float16(x - float(hi));
-        }
-#pragma unroll
-      for (int n = 0; n < kVL; ++n)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const h8_t v8 = u ? codes_f16<kFmt>(vc[n].z, vc[n].w) : codes_f16<kFmt>(vc[n].x, vc[n].y);
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            f32x4_t& o = st.o[rt][2 * n + u];
-            if (apart) {
-              f32x4_t x = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int np = 0; np < NP; ++np)
-                x = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, pp[rt][np], x, 0, 0, 0);
-              o += x * ratio;
-            } else {
-#pragma unroll
-              for (int np = 0; np < NP; ++np)
-                o = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, pp[rt][np], o, 0, 0, 0);
-            }
+          for (int e = 0; e < 8; ++e) {
+            const _Float16 hi = _Float16(z[rt][e]);
+            pp[rt][0][e] = hi;
+            if constexpr (kF32) pp[rt][NP - 1][e] = _Float16(z[rt][e] - float(hi));
           }
-        }
+#pragma unroll
+        for (int n = 0; n < kVL; ++n)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const h8_t v8 = u ? codes_f16<kFmt>(vr[n].z, vr[n].w) : codes_f16<kFmt>(vr[n].x, vr[n].y);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+              for (int np = 0; np < NP; ++np)
+                st.o[rt][2 * n + u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, pp[rt][np],
+                                                                           st.o[rt][2 * n + u], 0, 0, 0);
+          }
+        if (i + 1 < n8) load_v(i + 1);
+      }
     }
-    if (w0 <= full && full < w1) {
+    if (w0 <= full && full < w1 && full * kBlock < job.len) {
       // The tail: up to 31 rows in the call's own type.  bf16 rows use bf16
       // MFMAs (q as it is, p in two terms), fp32 rows fp32 MFMAs.
       const int nt = job.len - full * kBlock;
-      const char* kt = static_cast<const char*>(a.c.k_tail) + int64_t(job.unit) * kBlock * D * E::kBytes;
-      const char* vt = static_cast<const char*>(a.c.v_tail) + int64_t(job.unit) * kBlock * D * E::kBytes;
+      const int64_t tail_at = int64_t(unit) * kBlock * D * E::kBytes;
+      const Buf kt(static_cast<const char*>(a.c.k_tail) + tail_at, kBlock * D * E::kBytes);
+      const Buf vt(static_cast<const char*>(a.c.v_tail) + tail_at, kBlock * D * E::kBytes);
+      const int k_at = ((c16 / 4) * 8 + c16 % 4) * D * E::kBytes;
+      const int v_at = (g * D + 2 * c16) * 8 * E::kBytes;
       f32x4_t s[RT][2];
+      float t[RT];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      // (K rows past the tail's count give logits that are masked.)
-      if constexpr (!kF32) {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const char* p = q_row(rt);
+      for (int rt = 0; rt < RT; ++rt) {
+        s[rt][0] = s[rt][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        t[rt] = fmaxf(a.scale_log2, 0x1p-126f);
+        const int r = row0 + rt * 16 + c16;   // rows past the last repeat it; they are not written
+        const char* src = static_cast<const char*>(a.q.p) + row_offset<kF32>(a, a.q, job, h, min(r, job.rows - 1));
+        if constexpr (!kF32) {
 #pragma unroll
           for (int c = 0; c < kC; ++c) {
             const int d = 64 * (c / 2) + 16 * g + 8 * (c % 2);
-            uint4 qw = make_uint4(0, 0, 0, 0);
-            if (p != nullptr) qw = *reinterpret_cast<const uint4*>(p + d * 2);
+            const uint4 qw = *reinterpret_cast<const uint4*>(src + d * 2);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              const int t = (c16 / 4) * 8 + u * 4 + c16 % 4;
-              const uint4 kw = *reinterpret_cast<const uint4*>(kt + (t * D + d) * 2);
-              s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, kw),
-                                                               __builtin_bit_cast(bf16x8_t, qw), s[rt][u],
-                                                               0, 0, 0);
+              const uint4 kw = kt.ld16(k_at + u * 4 * D * 2 + d * 2);
+              s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  __builtin_bit_cast(bf16x8_t, kw), __builtin_bit_cast(bf16x8_t, qw), s[rt][u], 0, 0, 0);
             }
           }
-        }
-      } else {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const char* p = q_row(rt);
+        } else {
           for (int c = 0; c < D / 16; ++c) {
             const int d = 16 * c + 4 * g;
-            float4 qw = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (p != nullptr) qw = *reinterpret_cast<const float4*>(p + d * 4);
+            const float4 qw = *reinterpret_cast<const float4*>(src + d * 4);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              const int t = (c16 / 4) * 8 + u * 4 + c16 % 4;
-              const float4 kw = *reinterpret_cast<const float4*>(kt + (t * D + d) * 4);
+              const float4 kw = __builtin_bit_cast(float4, kt.ld16(k_at + u * 4 * D * 4 + d * 4));
               s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x4f32(kw.x, qw.x, s[rt][u], 0, 0, 0);
               s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x4f32(kw.y, qw.y, s[rt][u], 0, 0, 0);
               s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x4f32(kw.z, qw.z, s[rt][u], 0, 0, 0);
@@ -365,26 +500,21 @@ __global__ __launch_bounds__(256) void attn_kernel(PagedArgs a) {
             }
           }
         }
+        // Rows past the tail's count may hold anything.
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (8 * g + e >= nt || full * kBlock + 8 * g + e > seen[rt]) s[rt][e / 4][e % 4] = -__builtin_inff();
       }
-      float z[RT][8];
-      auto logit = [&](int rt, int e) {
-        const int t = 8 * g + e;
-        return t >= nt || full * kBlock + t > seen[rt] ? -__builtin_inff()
-                                                      : s[rt][e / 4][e % 4] * a.scale_log2;
-      };
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[rt][e] = logit(rt, e) - (st.m[rt] - kHead);
-      float ratio;
-      settle<D, RT>(st, z, 1.f, ratio, logit);
+      float p[RT][8];
+      exponentiate<D, RT>(st, exponents<D, RT>(st, s, t, 1.f, 0.f, kLeastTail, p), p);
 #pragma unroll
       for (int n = 0; n < D / 32; ++n)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          // Rows past the count may hold anything: zeros go into the product.
+          // Zeros where no row is: whatever lies there must not meet p = 0.
           float v[8];
-          E::load8(vt + (g * D + 32 * n + 2 * c16 + u) * 8 * E::kBytes, v);
+          const int at = v_at + (32 * n + u) * 8 * E::kBytes;
+          E::unpack8(vt.ld16(at), kF32 ? vt.ld16(at + 16) : uint4{}, v);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = 8 * g + e < nt ? v[e] : 0.f;
 #pragma unroll
@@ -393,7 +523,7 @@ __global__ __launch_bounds__(256) void attn_kernel(PagedArgs a) {
               bf16x8_t v8, hi, lo;
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float x = z[rt][e] * ratio;
+                const float x = p[rt][e];
                 v8[e] = __bf16(v[e]);
                 hi[e] = __bf16(x);
                 lo[e] = __bf16(x - float(hi[e]));
@@ -406,170 +536,182 @@ __global__ __launch_bounds__(256) void attn_kernel(PagedArgs a) {
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 st.o[rt][2 * n + u] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                    v[e], z[rt][e] * ratio, st.o[rt][2 * n + u], 0, 0, 0);
+                    v[e], p[rt][e], st.o[rt][2 * n + u], 0, 0, 0);
             }
           }
         }
     }
-  }
 
-  // ---- merge the four wavefronts ----
-  constexpr int kRows = RT * 16;
-  __shared__ float sm[4][kRows], sl[4][kRows];
-  __shared__ f32x4_t so[2][RT * (D / 16)][64];
+    // ---- merge the wavefronts ----
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    st.l[rt] += __shfl_xor(st.l[rt], 16, 64);
-    st.l[rt] += __shfl_xor(st.l[rt], 32, 64);
-    if (g == 0) {
-      sm[wave][rt * 16 + c16] = st.m[rt];
-      sl[wave][rt * 16 + c16] = st.l[rt];
-    }
-  }
-  __syncthreads();
-  float mx[RT], lsum[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int r = rt * 16 + c16;
-    mx[rt] = fmaxf(fmaxf(sm[0][r], sm[1][r]), fmaxf(sm[2][r], sm[3][r]));
-    lsum[rt] = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) lsum[rt] += sl[w][r] * exp2f(sm[w][r] - mx[rt]);
-    const float f = exp2f(st.m[rt] - mx[rt]) * st.vref;
-#pragma unroll
-    for (int n = 0; n < D / 16; ++n) st.o[rt][n] *= f;
-  }
-  auto put = [&](int at) {
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int n = 0; n < D / 16; ++n) so[at][rt * (D / 16) + n][lane] = st.o[rt][n];
-  };
-  auto add = [&](int at) {
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int n = 0; n < D / 16; ++n) st.o[rt][n] += so[at][rt * (D / 16) + n][lane];
-  };
-  if (wave >= 2) put(wave - 2);
-  __syncthreads();
-  if (wave < 2) add(wave);
-  __syncthreads();
-  if (wave == 1) put(0);
-  __syncthreads();
-  if (wave != 0) return;
-  add(0);
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int r = row0 + rt * 16 + c16;
-    if (r >= job.rows) continue;
-    if (a.n_splits == 1) {
-      const int i = r / a.group, gh = r - i * a.group;
-      const float inv = lsum[rt] == 0.f ? 0.f : 1.f / lsum[rt];
-      char* dst = static_cast<char*>(a.out.p) +
-                  ((job.q0 + i) * a.out.row_stride + (int64_t(h) * a.group + gh) * a.out.head_stride) *
-                      E::kBytes;
-#pragma unroll
-      for (int n = 0; n < D / 32; ++n) {
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[2 * e] = st.o[rt][2 * n][e] * inv;
-          x[2 * e + 1] = st.o[rt][2 * n + 1][e] * inv;
-        }
-        E::store8(dst + (32 * n + 8 * g) * E::kBytes, x);
-      }
-      if (a.lse != nullptr && g == 0)
-        a.lse[(job.q0 + i) * a.c.n_q_heads + h * a.group + gh] =
-            lsum[rt] == 0.f ? -__builtin_inff() : 0.69314718056f * (mx[rt] - kHead + log2f(lsum[rt]));
-    } else {
-      const int64_t pr =
-          ((int64_t(job.unit) * a.n_rt + rt0) * a.n_splits + split) * kRows + rt * 16 + c16;
-      float* dst = a.part_o + pr * D;
-#pragma unroll
-      for (int n = 0; n < D / 32; ++n) {
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[2 * e] = st.o[rt][2 * n][e];
-          x[2 * e + 1] = st.o[rt][2 * n + 1][e];
-        }
-        Elem<true>::store8(dst + 32 * n + 8 * g, x);
-      }
+    for (int rt = 0; rt < RT; ++rt) {
+      st.l[rt] += __shfl_xor(st.l[rt], 16, 64);
+      st.l[rt] += __shfl_xor(st.l[rt], 32, 64);
       if (g == 0) {
-        a.part_ml[2 * pr] = mx[rt];
-        a.part_ml[2 * pr + 1] = lsum[rt];
+        sb[wave][rt * 16 + c16] = st.base[rt];
+        sl[wave][rt * 16 + c16] = st.l[rt];
       }
     }
+    __syncthreads();
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int r = rt * 16 + c16;
+      float bmin = sb[0][r];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) bmin = fminf(bmin, sb[w][r]);
+      const float f = exp2f(bmin - st.base[rt]) * st.vref;
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) st.o[rt][n] *= f;
+    }
+    // Each wavefront leaves its o in LDS and sums its part of the columns.
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) so[wave][rt * (D / 16) + n][lane] = st.o[rt][n];
+    __syncthreads();
+
+    // ---- the result, or a partial ----
+    const int first = unit_at / share.size, last = (unit_at + job.n_blk - 1) / share.size;
+    constexpr int kParts = RT * (D / 32);      // (row tile, 32 columns) pairs
+#pragma unroll
+    for (int k = 0; k < (kParts + kWaves - 1) / kWaves; ++k) {
+      const int part = k * kWaves + wave;
+      if (kParts % kWaves != 0 && part >= kParts) break;
+      const int rt = part / (D / 32), n = part % (D / 32);
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        f32x4_t o = so[0][2 * part + u][lane];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) o += so[w][2 * part + u][lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[2 * e + u] = o[e];
+      }
+      const int r = row0 + rt * 16 + c16;
+      if (r >= job.rows) continue;
+      const int rr = rt * 16 + c16;
+      float bmin = sb[0][rr];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) bmin = fminf(bmin, sb[w][rr]);
+      float l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) l += sl[w][rr] * exp2f(bmin - sb[w][rr]);
+      if (first == last) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= inv;
+        E::store8(static_cast<char*>(a.out.p) + row_offset<kF32>(a, a.out, job, h, r) +
+                      (32 * n + 8 * g) * E::kBytes, x);
+        if (a.lse != nullptr && g == 0 && n == 0) write_lse(a, job, h, r, l, bmin);
+      } else {
+        const int64_t pr = (part_slot(share, unit_at, wg) * a.n_rt + rt0) * kRows + rr;
+        Elem<true>::store8(a.part_o + pr * D + 32 * n + 8 * g, x);
+        if (g == 0 && n == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * pr) = make_float2(bmin, l);
+      }
+    }
+    // The head's first piece says where its pieces are, in the first row
+    // tile's name (the cut is the same for all).
+    if (!kWhole && b0 == 0 && rt0 == 0 && threadIdx.x == 0)
+      a.pieces[unit] = first == last ? make_int2(0, 0)
+                                     : make_int2(last - first + 1, int(part_slot(share, unit_at, first)));
+    __syncthreads();   // LDS is reused by the next piece
   }
 }
 
-// Merges the splits of one query row: a workgroup per (row, unit), each
-// wavefront a quarter of the splits, D / 2 lanes two elements each.
+// Merges the pieces of one query row of one head, in order: D / 4 lanes a
+// piece, the workgroup's 256 / (D / 4) lane groups take every so manyth piece.
 template <int D, bool kF32>
-__global__ __launch_bounds__(256) void attn_combine_kernel(PagedArgs a, int tile) {
+__global__ __launch_bounds__(256) void attn_merge_kernel(PagedArgs a, int tile) {
   using E = Elem<kF32>;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const Job job = make_job(a, blockIdx.y, 0, 0);
-  const int r = blockIdx.x;
-  if (!job.ok || r >= job.rows) return;
-  const int n = max(1, min(a.n_splits, (job.n_blk + a.chunk - 1) / a.chunk));
-  const int rt0 = r / tile;
-  const int64_t p0 = (int64_t(job.unit) * a.n_rt + rt0) * a.n_splits * tile + (r - rt0 * tile);
-  float mx = kNoMax;
-  for (int s = lane; s < n; s += 64) mx = fmaxf(mx, a.part_ml[2 * (p0 + int64_t(s) * tile)]);
-  mx = fmaxf(half_max(mx), __shfl_xor(half_max(mx), 32, 64));
-  float l = 0.f, x = 0.f, y = 0.f;
-  for (int s = wave; s < n; s += 4) {
-    const int64_t p = p0 + int64_t(s) * tile;
-    const float f = exp2f(a.part_ml[2 * p] - mx);
-    l += a.part_ml[2 * p + 1] * f;
-    if (lane < D / 2) {
-      const float2 o = *reinterpret_cast<const float2*>(a.part_o + p * D + 2 * lane);
-      x += o.x * f;
-      y += o.y * f;
+  constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
+  const int unit = blockIdx.y, r = blockIdx.x, tid = threadIdx.x;
+  const int2 pieces = a.pieces[unit];   // (count, slot of the first); not written without queries
+  const Job job = make_job(a, unit);
+  if (r >= job.rows || pieces.x == 0) return;
+  const int grp = tid / kLanes, col = 4 * (tid % kLanes);
+  const int rt = r / tile;
+  // The first piece may lie in its share's second slot, the others in the first.
+  auto row_of = [&](int i) {
+    const int64_t slot = i == 0 ? pieces.y : (pieces.y & ~1) + 2 * i;
+    return (slot * a.n_rt + rt) * tile + (r - rt * tile);
+  };
+  float base = kNoBase, l = 0.f;
+  f32x4_t o = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  constexpr int kAhead = 4;
+  for (int i0 = grp; i0 < pieces.x; i0 += kGroups * kAhead) {
+    float2 ml[kAhead];
+    f32x4_t x[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t pr = row_of(min(i0 + i * kGroups, pieces.x - 1));
+      ml[i] = *reinterpret_cast<const float2*>(a.part_ml + 2 * pr);
+      x[i] = *reinterpret_cast<const f32x4_t*>(a.part_o + pr * D + col);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i * kGroups >= pieces.x) break;
+      const float b = fminf(base, ml[i].x);
+      const float f = exp2f(b - base), fi = exp2f(b - ml[i].x);
+      base = b;
+      l = l * f + ml[i].y * fi;
+      o = o * f + x[i] * fi;
     }
   }
-  __shared__ float red[3][4][64];
-  red[0][wave][lane] = l;
-  red[1][wave][lane] = x;
-  red[2][wave][lane] = y;
+  __shared__ float sb[kGroups], sl[kGroups];
+  __shared__ f32x4_t so[kGroups][kLanes];
+  if (tid % kLanes == 0) {
+    sb[grp] = base;
+    sl[grp] = l;
+  }
+  so[grp][tid % kLanes] = o;
   __syncthreads();
-  if (wave != 0) return;
-  l = (red[0][0][lane] + red[0][1][lane]) + (red[0][2][lane] + red[0][3][lane]);
-  x = (red[1][0][lane] + red[1][1][lane]) + (red[1][2][lane] + red[1][3][lane]);
-  y = (red[2][0][lane] + red[2][1][lane]) + (red[2][2][lane] + red[2][3][lane]);
-  const int i = r / a.group, gh = r - i * a.group, h = job.unit % a.c.n_kv_heads;
+  if (grp != 0) return;
+  float bmin = sb[0];
+#pragma unroll
+  for (int k = 1; k < kGroups; ++k) bmin = fminf(bmin, sb[k]);
+  l = 0.f;
+  o = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) {
+    const float f = exp2f(bmin - sb[k]);
+    l += sl[k] * f;
+    o += so[k][tid % kLanes] * f;
+  }
+  const int h = unit % a.c.n_kv_heads;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  if (lane < D / 2)
-    E::store2(static_cast<char*>(a.out.p) +
-                  ((job.q0 + i) * a.out.row_stride + (int64_t(h) * a.group + gh) * a.out.head_stride +
-                   2 * lane) * E::kBytes,
-              x * inv, y * inv);
-  if (a.lse != nullptr && lane == 0)
-    a.lse[(job.q0 + i) * a.c.n_q_heads + h * a.group + gh] =
-        l == 0.f ? -__builtin_inff() : 0.69314718056f * (mx - kHead + log2f(l));
+  char* dst = static_cast<char*>(a.out.p) + row_offset<kF32>(a, a.out, job, h, r) + col * E::kBytes;
+  E::store2(dst, o[0] * inv, o[1] * inv);
+  E::store2(dst + 2 * E::kBytes, o[2] * inv, o[3] * inv);
+  if (a.lse != nullptr && tid == 0) write_lse(a, job, h, r, l, bmin);
 }
 
 template <int D, bool kF32, int kFmt>
 hipError_t launch(const PagedArgs& a, hipStream_t s) {
   const int units = a.c.n_seqs * a.c.n_kv_heads;
-  const dim3 grid(uint32_t(a.n_splits * a.n_rt), units);
-  const int tile = paged_tile_rows(int64_t(a.max_q) * a.group, a.c.dtype);
-  if (tile == 16) hipLaunchKernelGGL((attn_kernel<D, kF32, kFmt, 1>), grid, dim3(256), 0, s, a);
-  else if (tile == 32) hipLaunchKernelGGL((attn_kernel<D, kF32, kFmt, 2>), grid, dim3(256), 0, s, a);
-  else if constexpr (!kF32) hipLaunchKernelGGL((attn_kernel<D, kF32, kFmt, 4>), grid, dim3(256), 0, s, a);
-  if (a.n_splits > 1)
-    hipLaunchKernelGGL((attn_combine_kernel<D, kF32>), dim3(uint32_t(a.max_q) * a.group, units),
-                       dim3(256), 0, s, a, tile);
+  const int tile = paged_tile_rows(int64_t(a.max_q) * a.group);
+  if (a.whole) {
+    const dim3 grid(uint32_t(units) * a.n_rt);
+    if (tile == 16)
+      hipLaunchKernelGGL((attn_kernel<D, kF32, kFmt, 1, false, true, 8>), grid, dim3(512), 0, s, a);
+    else
+      hipLaunchKernelGGL((attn_kernel<D, kF32, kFmt, 2, false, true, 4>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+  const dim3 grid(uint32_t(a.n_wg) * a.n_rt);
+  if (tile == 16 && a.stream_nt)
+    hipLaunchKernelGGL((attn_kernel<D, kF32, kFmt, 1, true, false, 4>), grid, dim3(256), 0, s, a);
+  else if (tile == 16)
+    hipLaunchKernelGGL((attn_kernel<D, kF32, kFmt, 1, false, false, 4>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((attn_kernel<D, kF32, kFmt, 2, false, false, 4>), grid, dim3(256), 0, s, a);
+  hipLaunchKernelGGL((attn_merge_kernel<D, kF32>), dim3(uint32_t(a.max_q) * a.group, units), dim3(256), 0, s, a,
+                     tile);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int paged_tile_rows(int64_t rows, int dtype) {
-  return rows <= 16 ? 16 : rows <= 32 || dtype == NX_F32 ? 32 : 64;
-}
+int paged_tile_rows(int64_t rows) { return rows <= 16 ? 16 : 32; }
 
 hipError_t launch_paged_attn(const PagedArgs& a, hipStream_t s) {
   const bool f32 = a.c.dtype == NX_F32, i8 = a.c.format == NX_CACHE_I8;
