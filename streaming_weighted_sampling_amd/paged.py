@@ -13,59 +13,63 @@ from dataclasses import dataclass, field
 
 import torch
 
-from ._lib import (NX_CACHE_BLOCK, NX_CACHE_E4M3, NX_CACHE_I8, NX_ROPE_HALF, NX_ROPE_PAIRS, NxPaged,
-                   NxRope, NxRows, check, load)
+from ._lib import (NX_CACHE_BLOCK, NX_CACHE_E4M3, NX_CACHE_I8, NX_ROPE_HALF, NX_ROPE_PAIRS, NxDesc,
+                   NxPaged, NxRope, NxRows, check, load)
 from .api import _DTYPES, NexusConfig
 
 _FORMATS = {torch.float8_e4m3fn: NX_CACHE_E4M3, torch.int8: NX_CACHE_I8}
 _NAMES = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
 
 
-def _tensor(t, name, shape, dtype, device=None):
-    """Checks a whole contiguous tensor; returns its address."""
+# The checks run on every call of a decode step, whose kernels take a few
+# microseconds: one comparison of each property, the message made only on failure.
+
+def _bad(t, name, shape, dtype, index):
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected contiguous {tuple(shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the cache or the queries are not")
+    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}, contiguous")
+
+
+def _tensor(t, name, shape, dtype, index):
+    """Address of a whole contiguous tensor."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _bad(t, name, shape, dtype, index)
     return t.data_ptr()
 
 
-def _opt(t, name, shape, dtype, device):
-    return None if t is None else _tensor(t, name, shape, dtype, device)
+def _opt(t, name, shape, dtype, index):
+    return None if t is None else _tensor(t, name, shape, dtype, index)
 
 
-def _rows(cfg, t, name, heads, device, n_rows=None):
-    """NxRows of a [rows, heads, head_dim] tensor with any row and head strides."""
-    if t.dtype != cfg.dtype:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {cfg.dtype}")
-    shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != cfg.head_dim or \
-            (n_rows is not None and shape[0] != n_rows):
-        raise ValueError(f"{name}: shape {tuple(shape)}, expected "
-                         f"[{'rows' if n_rows is None else n_rows}, {heads}, {cfg.head_dim}]")
-    s0, s1, s2 = t.stride()
-    if s2 != 1:
+def _rows(cfg, t, name, heads, index, n):
+    """NxRows of an [n, heads, head_dim] tensor with any row and head strides."""
+    if t.dtype is not cfg.dtype or t.shape != (n, heads, cfg.head_dim) or t.get_device() != index:
+        _bad(t, name, (n, heads, cfg.head_dim), cfg.dtype, index)
+    row, head, elem = t.stride()
+    if elem != 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return NxRows(t.data_ptr(), s0, s1)
+    return NxRows(t.data_ptr(), row, head)
 
 
-def _call(device, stream, set_stream, fn):
-    """Runs fn with `device` current and set_stream(handle) done."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a GPU, got {device}")
-    if torch.cuda.current_device() == device.index:
-        set_stream((stream or torch.cuda.current_stream()).cuda_stream)
-        return fn()
-    with torch.cuda.device(device):
-        set_stream((stream or torch.cuda.current_stream()).cuda_stream)
-        return fn()
+def _stream(stream, index):
+    """Handle of the given stream, or of the current one of GPU `index`."""
+    if index < 0:
+        raise ValueError("the tensors must be on a GPU")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on GPU {index}")
+    return stream.cuda_stream
+
+
+def _run(index, fn, *args):
+    """fn with GPU `index` current."""
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
 
 
 @dataclass
@@ -80,12 +84,13 @@ class Rope:
         if t.dim() != 2 or t.dtype != torch.float32 or not t.is_contiguous():
             raise ValueError("cos_sin must be a contiguous float32 [n_pos, rot_dim] tensor")
 
-    def _struct(self, positions, n_rows, device):
+    def _struct(self, positions, n_rows, index):
         t = self.cos_sin
-        if t.device != device:
-            raise ValueError(f"cos_sin is on {t.device}, expected {device}")
-        return NxRope(t.data_ptr(), _opt(positions, "positions", (n_rows,), torch.int32, device),
-                      t.shape[0], t.shape[1], NX_ROPE_PAIRS if self.pairs else NX_ROPE_HALF)
+        if t.get_device() != index:
+            raise ValueError(f"cos_sin is on {t.device}, the rows are not")
+        n_pos, rot = t.shape
+        return NxRope(t.data_ptr(), _opt(positions, "positions", (n_rows,), torch.int32, index), n_pos, rot,
+                      NX_ROPE_PAIRS if self.pairs else NX_ROPE_HALF)
 
 
 def rope_table(n_pos, rot_dim, base=10000.0, *, inv_freq=None, first=0, device="cuda"):
@@ -127,14 +132,14 @@ class PagedCache:
                              "[n_seqs, n_kv_heads, max_pages]")
         n_pages, blocks = self.k_codes.shape[:2]
         n_seqs, _, max_pages = self.table.shape
-        dev, f8 = self.k_codes.device, self.k_codes.dtype
-        self.device, self.n_seqs = dev, n_seqs
+        dev, f8 = self.k_codes.get_device(), self.k_codes.dtype
+        self.device, self.n_seqs, self._index = self.k_codes.device, n_seqs, dev
         self.capacity = max_pages * blocks * NX_CACHE_BLOCK      # rows that a head's table can hold
         c = NxPaged()
         c.n_seqs, c.n_q_heads, c.n_kv_heads, c.head_dim = n_seqs, cfg.n_q_heads, hk, d
         c.dtype, c.format = _DTYPES.get(cfg.dtype, 99), _FORMATS[f8]
         c.page_blocks, c.n_pages, c.max_pages = blocks, n_pages, max_pages
-        c.k_codes = _tensor(self.k_codes, "k_codes", (n_pages, blocks, NX_CACHE_BLOCK, d), f8)
+        c.k_codes = _tensor(self.k_codes, "k_codes", (n_pages, blocks, NX_CACHE_BLOCK, d), f8, dev)
         c.v_codes = _tensor(self.v_codes, "v_codes", (n_pages, blocks, 4, d, 8), f8, dev)
         c.k_scale = _tensor(self.k_scale, "k_scale", (n_pages, blocks), torch.float32, dev)
         c.v_scale = _tensor(self.v_scale, "v_scale", (n_pages, blocks), torch.float32, dev)
@@ -144,15 +149,16 @@ class PagedCache:
         c.lens = _tensor(self.lens, "lens", (n_seqs, hk), torch.int32, dev)
         self._c = c
 
-    def _struct(self, cfg, workspace):
+    def _struct(self, cfg, workspace, stream):
         if cfg is not self.cfg and cfg != self.cfg:
             raise ValueError("the cache was made for another configuration")
-        if workspace.device != self.device or not workspace.is_contiguous():
+        if workspace.get_device() != self._index or not workspace.is_contiguous():
             raise ValueError(f"the workspace must be contiguous on {self.device}")
         # A copy: calls from several threads share the cache object.
         c = NxPaged.from_buffer_copy(self._c)
         c.workspace = workspace.data_ptr()
-        c.workspace_bytes = workspace.numel() * workspace.element_size()
+        c.workspace_bytes = workspace.nbytes
+        c.stream = _stream(stream, self._index)
         return c
 
 
@@ -198,35 +204,42 @@ def nx_qk_norm_rope(cfg, q, k=None, *, workspace, q_weight=None, k_weight=None, 
     A side without a weight is rotated only; rope None: no rotation.  Outputs
     may be views with other strides (a query window, a cache's append rows) or
     the inputs themselves."""
-    dev, n = q.device, q.shape[0]
-    rq = _rows(cfg, q, "q", cfg.n_q_heads, dev)
+    dev, n, hq, hk, d = q.get_device(), q.shape[0], cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim
+    rq = _rows(cfg, q, "q", hq, dev, n)
     if out_q is None:
-        out_q = torch.empty(n, cfg.n_q_heads, cfg.head_dim, dtype=cfg.dtype, device=dev)
-    roq = _rows(cfg, out_q, "out_q", cfg.n_q_heads, dev, n)
+        out_q = torch.empty(n, hq, d, dtype=cfg.dtype, device=q.device)
+    roq = _rows(cfg, out_q, "out_q", hq, dev, n)
     rk = rok = None
     if k is not None:
-        rk = _rows(cfg, k, "k", cfg.n_kv_heads, dev, n)
+        rk = _rows(cfg, k, "k", hk, dev, n)
         if out_k is None:
-            out_k = torch.empty(n, cfg.n_kv_heads, cfg.head_dim, dtype=cfg.dtype, device=dev)
-        rok = _rows(cfg, out_k, "out_k", cfg.n_kv_heads, dev, n)
+            out_k = torch.empty(n, hk, d, dtype=cfg.dtype, device=q.device)
+        rok = _rows(cfg, out_k, "out_k", hk, dev, n)
     elif out_k is not None:
         raise ValueError("out_k without k")
-    wq = _opt(q_weight, "q_weight", (cfg.head_dim,), cfg.dtype, dev)
-    wk = _opt(k_weight, "k_weight", (cfg.head_dim,), cfg.dtype, dev)
+    wq = _opt(q_weight, "q_weight", (d,), cfg.dtype, dev)
+    wk = _opt(k_weight, "k_weight", (d,), cfg.dtype, dev)
     if rope is None and positions is not None:
         raise ValueError("positions without rope")
     r = None if rope is None else rope._struct(positions, n, dev)
-    if workspace.device != dev:
-        raise ValueError(f"the workspace must be on {dev}")
-    d = cfg.desc(workspace)
-    lib = load()
-
-    def set_stream(s):
-        d.stream = s
-
-    check(_call(dev, stream, set_stream,
-                lambda: lib.nx_qk_norm_rope(d, r, n, rq, roq, wq, rk, rok, wk, eps)), "nx_qk_norm_rope")
+    if workspace.get_device() != dev:
+        raise ValueError(f"the workspace must be on {q.device}")
+    c = NxDesc()
+    c.n_q_heads, c.n_kv_heads, c.head_dim, c.dtype = hq, hk, d, _DTYPES.get(cfg.dtype, 99)
+    c.workspace, c.workspace_bytes, c.stream = workspace.data_ptr(), workspace.nbytes, _stream(stream, dev)
+    check(_run(dev, load().nx_qk_norm_rope, c, r, n, rq, roq, wq, rk, rok, wk, eps), "nx_qk_norm_rope")
     return out_q, out_k
+
+
+def _per_seq(cache, n, most, starts, most_name, starts_name):
+    """The given bound on a sequence's rows, or the even division of n rows."""
+    if most is not None:
+        return most
+    if starts is not None:
+        raise ValueError(f"{starts_name} needs {most_name}")
+    if n % cache.n_seqs:
+        raise ValueError(f"{n} rows do not divide into {cache.n_seqs} sequences")
+    return n // cache.n_seqs
 
 
 def nx_paged_append(cfg, cache, k, v, *, workspace, max_new=None, new_start=None, head_new=None,
@@ -236,29 +249,18 @@ def nx_paged_append(cfg, cache, k, v, *, workspace, max_new=None, new_start=None
     new_start: int32 [n_seqs + 1] first rows of the sequences (None: max_new rows each,
     default rows // n_seqs); head_new: int32 [n_seqs, n_kv_heads] rows each head takes of
     its sequence's; lens_out: int32 [n_seqs, n_kv_heads] (None: cache.lens is advanced)."""
-    dev, n, hk = cache.device, k.shape[0], cfg.n_kv_heads
-    rk = _rows(cfg, k, "k", hk, dev)
+    dev, n, hk, s = cache._index, k.shape[0], cfg.n_kv_heads, cache.n_seqs
+    rk = _rows(cfg, k, "k", hk, dev, n)
     rv = _rows(cfg, v, "v", hk, dev, n)
-    if max_new is None:
-        if new_start is not None:
-            raise ValueError("new_start needs max_new")
-        if n % cache.n_seqs:
-            raise ValueError(f"{n} rows do not divide into {cache.n_seqs} sequences")
-        max_new = n // cache.n_seqs
-    ns = _opt(new_start, "new_start", (cache.n_seqs + 1,), torch.int32, dev)
-    hn = _opt(head_new, "head_new", (cache.n_seqs, hk), torch.int32, dev)
-    lo = _opt(lens_out, "lens_out", (cache.n_seqs, hk), torch.int32, dev)
+    max_new = _per_seq(cache, n, max_new, new_start, "max_new", "new_start")
+    ns = _opt(new_start, "new_start", (s + 1,), torch.int32, dev)
+    hn = _opt(head_new, "head_new", (s, hk), torch.int32, dev)
+    lo = _opt(lens_out, "lens_out", (s, hk), torch.int32, dev)
     if rope is None and positions is not None:
         raise ValueError("positions without rope")
     r = None if rope is None else rope._struct(positions, n, dev)
-    c = cache._struct(cfg, workspace)
-    lib = load()
-
-    def set_stream(s):
-        c.stream = s
-
-    check(_call(dev, stream, set_stream,
-                lambda: lib.nx_paged_append(c, r, rk, rv, n, ns, hn, max_new, lo)), "nx_paged_append")
+    c = cache._struct(cfg, workspace, stream)
+    check(_run(dev, load().nx_paged_append, c, r, rk, rv, n, ns, hn, max_new, lo), "nx_paged_append")
 
 
 def nx_paged_attn(cfg, cache, q, *, workspace, max_tokens, max_q=None, q_start=None, scale=None,
@@ -268,29 +270,18 @@ def nx_paged_attn(cfg, cache, q, *, workspace, max_tokens, max_q=None, q_start=N
     q_start: int32 [n_seqs + 1] first query rows of the sequences (None: max_q each, default
     rows // n_seqs); max_tokens: the expected longest head (any value is correct, and the
     workspace must have been made for at least it); out_lse: float32 [rows, n_q_heads]."""
-    dev, n = cache.device, q.shape[0]
-    rq = _rows(cfg, q, "q", cfg.n_q_heads, dev)
+    dev, n, hq = cache._index, q.shape[0], cfg.n_q_heads
+    rq = _rows(cfg, q, "q", hq, dev, n)
     if out is None:
-        out = torch.empty(n, cfg.n_q_heads, cfg.head_dim, dtype=cfg.dtype, device=dev)
-    ro = _rows(cfg, out, "out", cfg.n_q_heads, dev, n)
-    if max_q is None:
-        if q_start is not None:
-            raise ValueError("q_start needs max_q")
-        if n % cache.n_seqs:
-            raise ValueError(f"{n} rows do not divide into {cache.n_seqs} sequences")
-        max_q = n // cache.n_seqs
+        out = torch.empty(n, hq, cfg.head_dim, dtype=cfg.dtype, device=q.device)
+    ro = _rows(cfg, out, "out", hq, dev, n)
+    max_q = _per_seq(cache, n, max_q, q_start, "max_q", "q_start")
     if scale is not None and not scale > 0:
         raise ValueError("scale must be positive")
     qs = _opt(q_start, "q_start", (cache.n_seqs + 1,), torch.int32, dev)
-    lse = _opt(out_lse, "out_lse", (n, cfg.n_q_heads), torch.float32, dev)
-    c = cache._struct(cfg, workspace)
-    lib = load()
-
-    def set_stream(s):
-        c.stream = s
-
-    check(_call(dev, stream, set_stream,
-                lambda: lib.nx_paged_attn(c, rq, ro, n, qs, max_tokens, max_q, scale or 0.0, lse)),
+    lse = _opt(out_lse, "out_lse", (n, hq), torch.float32, dev)
+    c = cache._struct(cfg, workspace, stream)
+    check(_run(dev, load().nx_paged_attn, c, rq, ro, n, qs, max_tokens, max_q, scale or 0.0, lse),
           "nx_paged_attn")
     return out
 
@@ -298,28 +289,21 @@ def nx_paged_attn(cfg, cache, q, *, workspace, max_tokens, max_q=None, q_start=N
 def nx_paged_gather(cfg, cache, *, workspace, max_tokens, out_k=None, out_v=None, stream=None):
     """The cached rows as [n_seqs, n_kv_heads, >= max_tokens, D] tensors (rows past a head's
     length are left as they were; new outputs are zero-filled); returns (out_k, out_v)."""
-    dev, hk, d = cache.device, cfg.n_kv_heads, cfg.head_dim
-    shape = (cache.n_seqs, hk, max_tokens, d)
+    shape, d = (cache.n_seqs, cfg.n_kv_heads, max_tokens, cfg.head_dim), cfg.head_dim
     if out_k is None:
-        out_k = torch.zeros(shape, dtype=cfg.dtype, device=dev)
+        out_k = torch.zeros(shape, dtype=cfg.dtype, device=cache.device)
     if out_v is None:
         out_v = torch.zeros_like(out_k)
     for t, name in ((out_k, "out_k"), (out_v, "out_v")):
-        if t.dtype != cfg.dtype:
-            raise TypeError(f"{name}: dtype {t.dtype}, expected {cfg.dtype}")
-        if t.dim() != 4 or t.shape[:2] != shape[:2] or t.shape[2] < max_tokens or t.shape[3] != d:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-        if t.stride(3) != 1 or t.stride(2) != d or t.device != dev:
-            raise ValueError(f"{name}: rows must be contiguous on {dev}")
+        got, st = t.shape, t.stride()
+        if t.dtype is not cfg.dtype or len(got) != 4 or got[:2] != shape[:2] or got[2] < max_tokens or \
+                got[3] != d or t.get_device() != cache._index:
+            _bad(t, name, shape, cfg.dtype, cache._index)
+        if st[3] != 1 or st[2] != d:
+            raise ValueError(f"{name}: rows must be contiguous")
     if out_k.stride() != out_v.stride():
         raise ValueError("out_k and out_v must share their strides")
-    c = cache._struct(cfg, workspace)
-    lib = load()
-
-    def set_stream(s):
-        c.stream = s
-
-    check(_call(dev, stream, set_stream,
-                lambda: lib.nx_paged_gather(c, max_tokens, out_k.data_ptr(), out_v.data_ptr(),
-                                            out_k.stride(0), out_k.stride(1))), "nx_paged_gather")
+    c = cache._struct(cfg, workspace, stream)
+    check(_run(cache._index, load().nx_paged_gather, c, max_tokens, out_k.data_ptr(), out_v.data_ptr(),
+               st[0], st[1]), "nx_paged_gather")
     return out_k, out_v
