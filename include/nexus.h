@@ -432,7 +432,7 @@ nx_status nx_qk_norm_rope(const nx_desc* desc, const nx_rope* rope, int32_t n_ro
 
 /*
  * Appends new K / V rows to every (sequence, head), K rotated on the way.
- *   k, v       n_rows rows of n_kv_heads heads
+ *   k, v       n_rows rows of n_kv_heads heads (a row stride of 64 MB or more: NX_EUNSUPPORTED)
  *   new_start  nullable [n_seqs + 1] int32 (device): sequence s appends rows new_start[s] ..
  *              new_start[s + 1] - 1, at most max_new; NULL: rows s * max_new ..
  *              (s + 1) * max_new - 1

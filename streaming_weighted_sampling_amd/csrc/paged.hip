@@ -18,11 +18,11 @@ __device__ inline Runs runs_of(int j, int rot_dim) {
   return {rot ? 8 * j : 16 * j, rot ? rot_dim / 2 + 8 * j : 16 * j + 8, rot};
 }
 
-// Table row of call row `row`; a position outside the table is reported and reads row 0.
-__device__ inline const float* table_row(const nx_rope& r, int64_t row, uint32_t* status) {
+// Table row of call row `row`; a position outside the table is noted and reads row 0.
+__device__ inline const float* table_row(const nx_rope& r, int64_t row, bool& off_table) {
   int64_t p = r.positions != nullptr ? int64_t(r.positions[row]) : row;
   if (p < 0 || p >= r.n_pos) {
-    paged_status(status, kStatusBadItem);
+    off_table = true;
     p = 0;
   }
   return r.cos_sin + p * r.rot_dim;
@@ -101,11 +101,12 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = y[i] * f * w[i];
   }
-  if (r.rot)
-    rotate_runs<float>(x, y, table_row(a.rope, row, a.status), j, a.rope.rot_dim, a.rope.style);
+  bool off_table = false;
+  if (r.rot) rotate_runs<float>(x, y, table_row(a.rope, row, off_table), j, a.rope.rot_dim, a.rope.style);
   char* dst = static_cast<char*>(out.p) + (row * out.row_stride + h * out.head_stride) * E::kBytes;
   E::store8(dst + r.d0 * E::kBytes, x);
   E::store8(dst + r.d1 * E::kBytes, y);
+  if (off_table) paged_status(a.status, kStatusBadItem);
 }
 
 // ---- append ----
@@ -145,6 +146,27 @@ __device__ inline float finite_or_zero(float x, bool& bad) {
   return f ? x : 0.f;
 }
 
+// Largest magnitude of a thread's elements, as bits.
+__device__ inline uint32_t top_bits(const float (&x)[8], const float (&y)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    m = max(m, max(__builtin_bit_cast(uint32_t, x[e]) & 0x7FFFFFFFu, __builtin_bit_cast(uint32_t, y[e]) & 0x7FFFFFFFu));
+  return m;
+}
+
+// The wavefront's maximum, in every lane (row shifts, row broadcasts, lane 63).
+__device__ inline uint32_t wave_top(uint32_t v) {
+  auto step = [&](int x) { v = max(v, uint32_t(x)); };
+  step(__builtin_amdgcn_update_dpp(0, int(v), 0x111, 0xF, 0xF, false));
+  step(__builtin_amdgcn_update_dpp(0, int(v), 0x112, 0xF, 0xF, false));
+  step(__builtin_amdgcn_update_dpp(0, int(v), 0x114, 0xF, 0xF, false));
+  step(__builtin_amdgcn_update_dpp(0, int(v), 0x118, 0xF, 0xF, false));
+  step(__builtin_amdgcn_update_dpp(0, int(v), 0x142, 0xA, 0xF, false));
+  step(__builtin_amdgcn_update_dpp(0, int(v), 0x143, 0xC, 0xF, false));
+  return uint32_t(__builtin_amdgcn_readlane(int(v), 63));
+}
+
 // 4 values -> 4 codes, round to nearest even.  |x| exceeds the largest code by
 // fp32 roundings at most, so neither conversion overflows.
 template <int kFmt>
@@ -153,10 +175,24 @@ __device__ inline uint32_t codes4(float a, float b, float c, float d) {
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
     return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
   } else {
-    const uint32_t x = uint32_t(int(rintf(a))) & 0xFFu, y = uint32_t(int(rintf(b))) & 0xFFu;
-    const uint32_t z = uint32_t(int(rintf(c))) & 0xFFu, t = uint32_t(int(rintf(d)));
-    return x | (y << 8) | (z << 16) | (t << 24);
+    // Adding 1.5 * 2^23 rounds to an integer, whose two's complement is then in
+    // the low bits; v_perm collects the low bytes.
+    constexpr float kRound = 12582912.f;
+    const uint32_t ab = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b + kRound),
+                                              __builtin_bit_cast(uint32_t, a + kRound), 0x0C0C0400u);
+    const uint32_t cd = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, d + kRound),
+                                              __builtin_bit_cast(uint32_t, c + kRound), 0x0C0C0400u);
+    return ab | (cd << 16);
   }
+}
+
+// The product is rounded by itself, as the definition has it: fused with the
+// rounding addition it would move ties.
+template <int kFmt>
+__device__ inline uint2 codes8(const float (&x)[8], float inv) {
+#pragma clang fp contract(off)
+  return make_uint2(codes4<kFmt>(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+                    codes4<kFmt>(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
 }
 
 // Scale and inverse of a block whose largest magnitude is `top`.
@@ -168,21 +204,28 @@ __device__ inline void block_scale(float top, float& scale, float& inv) {
   inv = zero ? 0.f : (1.f / top) * kTop;
 }
 
-// Workgroup (x, unit): block len / 32 + x of the (sequence, head) if the call
+// Workgroup (x, head) of a sequence: block len / 32 + x of the head if the call
 // fills it; x = 0 also writes the rows that stay in the tail, after it has read
 // the tail's old rows.  K: 16 elements of one row per thread (rotation pairs in
 // one thread).  V: 8 rows x 2 elements per thread, which is 16 consecutive
 // bytes of the stored block.
 template <int D, bool kF32, int kFmt>
-__global__ __launch_bounds__(256) void append_kernel(PagedArgs a) {
+__global__ __launch_bounds__(256, kF32 ? 4 : 6) void append_kernel(PagedArgs a) {
   using E = Elem<kF32>;
   constexpr int kLanes = D / 16;                 // K threads per row
   constexpr int kUse = 32 * kLanes;              // threads at work: 256 or 128
-  const int unit = blockIdx.y, tid = threadIdx.x;
-  const int h = unit % a.c.n_kv_heads;
+  const int tid = threadIdx.x, hk = a.c.n_kv_heads;
+  // The heads of one row range run side by side: their rows lie next to each
+  // other in a projection, and they share the rotation table's rows.  With
+  // eight ranges or more the heads of a range are eight workgroups apart, so on
+  // one XCD and its L2.
+  const int id = blockIdx.x;
+  const int nth = a.append_by8 ? id / (8 * hk) * 8 + id % 8 : id / hk;
+  const int h = a.append_by8 ? id % (8 * hk) / 8 : id % hk;
+  const int unit = blockIdx.y * hk + h;
   const Span p = append_span(a, unit);
   if (!p.ok) {
-    if (blockIdx.x == 0 && tid == 0) {
+    if (nth == 0 && tid == 0) {
       paged_status(a.status, kStatusBadItem);
       if (a.lens_out != a.c.lens) a.lens_out[unit] = a.c.lens[unit];
     }
@@ -190,75 +233,92 @@ __global__ __launch_bounds__(256) void append_kernel(PagedArgs a) {
   }
   const int end = p.len + p.n;
   const int first = p.len / kBlock, open = end / kBlock;
-  const int b = first + blockIdx.x;
-  const char* ks = static_cast<const char*>(a.k.p) + h * a.k.head_stride * E::kBytes;
-  const char* vs = static_cast<const char*>(a.v.p) + h * a.v.head_stride * E::kBytes;
+  const int b = first + nth;
   char* kt = static_cast<char*>(a.c.k_tail) + int64_t(unit) * kBlock * D * E::kBytes;
   char* vt = static_cast<char*>(a.c.v_tail) + int64_t(unit) * kBlock * D * E::kBytes;
   const int krow = tid / kLanes, kj = tid % kLanes;
   const Runs r = runs_of(kj, a.rope.rot_dim);
   const int vg = tid / (D / 2), vd = tid % (D / 2) * 2;
   const bool on = tid < kUse;
-  bool bad = false;
+  bool bad = false, off_table = false;
 
-  // Rotated and rounded K elements of new row i.
-  auto new_k = [&](int i, float (&x)[8], float (&y)[8]) {
-    const int64_t row = p.row0 + i;
-    const char* src = ks + row * a.k.row_stride * E::kBytes;
-    E::load8(src + r.d0 * E::kBytes, x);
-    E::load8(src + r.d1 * E::kBytes, y);
+  // Where new row i (uniform or per thread) starts.
+  auto k_at = [&](int64_t i) {
+    return static_cast<const char*>(a.k.p) + ((p.row0 + i) * a.k.row_stride + h * a.k.head_stride) * E::kBytes;
+  };
+  auto v_at = [&](int64_t i) {
+    return static_cast<const char*>(a.v.p) + ((p.row0 + i) * a.v.row_stride + h * a.v.head_stride) * E::kBytes;
+  };
+  // Rotates and rounds the K elements of new row i.
+  auto turn_k = [&](int i, float (&x)[8], float (&y)[8]) {
     if (r.rot)
-      rotate_runs<double>(x, y, table_row(a.rope, row, a.status), kj, a.rope.rot_dim, a.rope.style);
+      rotate_runs<double>(x, y, table_row(a.rope, p.row0 + i, off_table), kj, a.rope.rot_dim, a.rope.style);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      x[e] = finite_or_zero(E::round(x[e]), bad);
-      y[e] = finite_or_zero(E::round(y[e]), bad);
+      x[e] = E::round(x[e]);
+      y[e] = E::round(y[e]);
     }
   };
-  auto new_v = [&](int i, float& x, float& y) {
-    E::load2(vs + ((p.row0 + i) * a.v.row_stride + vd) * E::kBytes, x, y);
-    x = finite_or_zero(x, bad);
-    y = finite_or_zero(y, bad);
+  auto clear = [&](float (&x)[8], float (&y)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = finite_or_zero(x[e], bad);
+      y[e] = finite_or_zero(y[e], bad);
+    }
   };
 
   if (b < open) {   // this call fills block b (uniform over the workgroup)
     const int page = a.c.table[int64_t(unit) * a.c.max_pages + (b >> a.page_shift)];
     const bool page_ok = page >= 0 && page < a.c.n_pages;
-    float kx[8] = {}, ky[8] = {}, vx[16] = {};
+    float kx[8] = {}, ky[8] = {}, vx[8] = {}, vy[8] = {};
     if (on) {
-      const int t = b * kBlock + krow;
-      if (t < p.len) {
-        E::load8(kt + (krow * D + r.d0) * E::kBytes, kx);
-        E::load8(kt + (krow * D + r.d1) * E::kBytes, ky);
-      } else {
-        new_k(t - p.len, kx, ky);
-      }
+      const int new0 = b * kBlock - p.len;      // new row at the block's start (< 0: the tail's rows come first)
+      if (new0 >= 0) {
+        // Uniform bases, 32-bit offsets.  V's and K's loads are on their way
+        // before K waits for its table row.
+        const int vstep = int(a.v.row_stride) * E::kBytes;
+        const Buf vb(v_at(new0), 0x7FFFFFFF), kb(k_at(new0), 0x7FFFFFFF);
+        typename E::Pair w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int tv = b * kBlock + vg * 8 + i;
-        if (tv < p.len) {
-          const char* e = vt + ((vg * D + vd) * 8 + i) * E::kBytes;
-          if constexpr (kF32) {
-            vx[i] = *reinterpret_cast<const float*>(e);
-            vx[8 + i] = *reinterpret_cast<const float*>(e + 32);
-          } else {
-            vx[i] = float(*reinterpret_cast<const __bf16*>(e));
-            vx[8 + i] = float(*reinterpret_cast<const __bf16*>(e + 16));
-          }
+        for (int i = 0; i < 8; ++i) w[i] = E::ld_pair(vb, vg * 8 * vstep + vd * E::kBytes, i * vstep);
+        const int koff = krow * (int(a.k.row_stride) * E::kBytes);
+        E::unpack8(kb.ld16(koff + r.d0 * E::kBytes), kF32 ? kb.ld16(koff + r.d0 * E::kBytes + 16) : uint4{}, kx);
+        E::unpack8(kb.ld16(koff + r.d1 * E::kBytes), kF32 ? kb.ld16(koff + r.d1 * E::kBytes + 16) : uint4{}, ky);
+        turn_k(new0 + krow, kx, ky);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) E::split(w[i], vx[i], vy[i]);
+      } else {
+        const int t = new0 + krow, tv = new0 + vg * 8;
+        if (t < 0) {
+          E::load8(kt + (krow * D + r.d0) * E::kBytes, kx);
+          E::load8(kt + (krow * D + r.d1) * E::kBytes, ky);
         } else {
-          new_v(tv - p.len, vx[i], vx[8 + i]);
+          E::load8(k_at(t) + r.d0 * E::kBytes, kx);
+          E::load8(k_at(t) + r.d1 * E::kBytes, ky);
+          turn_k(t, kx, ky);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (tv + i < 0) {
+            vx[i] = E::load1(vt + ((vg * D + vd) * 8 + i) * E::kBytes);
+            vy[i] = E::load1(vt + ((vg * D + vd + 1) * 8 + i) * E::kBytes);
+          } else {
+            E::load2(v_at(tv + i) + vd * E::kBytes, vx[i], vy[i]);
+          }
         }
       }
     }
-    float km = 0.f, vm = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      km = fmaxf(km, fmaxf(fabsf(kx[i]), fabsf(ky[i])));
-      vm = fmaxf(vm, fmaxf(fabsf(vx[i]), fabsf(vx[8 + i])));
+    // Magnitudes are compared as integers, where NaN and infinity come last.
+    uint32_t km = top_bits(kx, ky), vm = top_bits(vx, vy);
+    if (__builtin_expect(max(km, vm) >= 0x7F800000u, 0)) {
+      clear(kx, ky);
+      clear(vx, vy);
+      km = top_bits(kx, ky);
+      vm = top_bits(vx, vy);
     }
-    km = fmaxf(half_max(km), __shfl_xor(half_max(km), 32, 64));
-    vm = fmaxf(half_max(vm), __shfl_xor(half_max(vm), 32, 64));
-    __shared__ float red[2][4];
+    km = wave_top(km);
+    vm = wave_top(vm);
+    __shared__ uint32_t red[2][4];
     if (tid % 64 == 0) {
       red[0][tid / 64] = km;
       red[1][tid / 64] = vm;
@@ -266,47 +326,37 @@ __global__ __launch_bounds__(256) void append_kernel(PagedArgs a) {
     // The maxima depend on every tail row read above, so past this barrier the
     // tail may be overwritten.
     __syncthreads();
-    km = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-    vm = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
+    const float ktop = __builtin_bit_cast(float, max(max(red[0][0], red[0][1]), max(red[0][2], red[0][3])));
+    const float vtop = __builtin_bit_cast(float, max(max(red[1][0], red[1][1]), max(red[1][2], red[1][3])));
     float kscale, kinv, vscale, vinv;
-    block_scale<kFmt>(km, kscale, kinv);
-    block_scale<kFmt>(vm, vscale, vinv);
+    block_scale<kFmt>(ktop, kscale, kinv);
+    block_scale<kFmt>(vtop, vscale, vinv);
     if (!page_ok) {
       if (tid == 0) paged_status(a.status, kStatusBadItem);
     } else if (on) {
       const int64_t slot = (int64_t(page) << a.page_shift) + (b & ((1 << a.page_shift) - 1));
       char* kc = static_cast<char*>(a.c.k_codes) + slot * kBlock * D;
       char* vc = static_cast<char*>(a.c.v_codes) + slot * kBlock * D;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        kx[i] *= kinv;
-        ky[i] *= kinv;
-        vx[i] *= vinv;
-        vx[8 + i] *= vinv;
-      }
-      const uint32_t k0 = codes4<kFmt>(kx[0], kx[1], kx[2], kx[3]);
-      const uint32_t k1 = codes4<kFmt>(kx[4], kx[5], kx[6], kx[7]);
-      const uint32_t k2 = codes4<kFmt>(ky[0], ky[1], ky[2], ky[3]);
-      const uint32_t k3 = codes4<kFmt>(ky[4], ky[5], ky[6], ky[7]);
-      *reinterpret_cast<uint2*>(kc + krow * D + r.d0) = make_uint2(k0, k1);
-      *reinterpret_cast<uint2*>(kc + krow * D + r.d1) = make_uint2(k2, k3);
-      *reinterpret_cast<uint4*>(vc + (vg * D + vd) * 8) =
-          make_uint4(codes4<kFmt>(vx[0], vx[1], vx[2], vx[3]), codes4<kFmt>(vx[4], vx[5], vx[6], vx[7]),
-                     codes4<kFmt>(vx[8], vx[9], vx[10], vx[11]),
-                     codes4<kFmt>(vx[12], vx[13], vx[14], vx[15]));
+      *reinterpret_cast<uint2*>(kc + krow * D + r.d0) = codes8<kFmt>(kx, kinv);
+      *reinterpret_cast<uint2*>(kc + krow * D + r.d1) = codes8<kFmt>(ky, kinv);
+      const uint2 v0 = codes8<kFmt>(vx, vinv), v1 = codes8<kFmt>(vy, vinv);
+      *reinterpret_cast<uint4*>(vc + (vg * D + vd) * 8) = make_uint4(v0.x, v0.y, v1.x, v1.y);
       if (tid == 0) {
         a.c.k_scale[slot] = kscale;
         a.c.v_scale[slot] = vscale;
       }
     }
   }
-  if (blockIdx.x == 0) {
+  if (nth == 0) {
     // New rows of the block that stays open.
     if (on) {
       const int t = open * kBlock + krow;
       if (t >= p.len && t < end) {
         float x[8], y[8];
-        new_k(t - p.len, x, y);
+        E::load8(k_at(t - p.len) + r.d0 * E::kBytes, x);
+        E::load8(k_at(t - p.len) + r.d1 * E::kBytes, y);
+        turn_k(t - p.len, x, y);
+        clear(x, y);
         E::store8(kt + (krow * D + r.d0) * E::kBytes, x);
         E::store8(kt + (krow * D + r.d1) * E::kBytes, y);
       }
@@ -315,16 +365,17 @@ __global__ __launch_bounds__(256) void append_kernel(PagedArgs a) {
         const int tv = open * kBlock + vg * 8 + i;
         if (tv >= p.len && tv < end) {
           float x, y;
-          new_v(tv - p.len, x, y);
+          E::load2(v_at(tv - p.len) + vd * E::kBytes, x, y);
           char* e = vt + ((vg * D + vd) * 8 + i) * E::kBytes;
-          E::store1(e, x);
-          E::store1(e + 8 * E::kBytes, y);
+          E::store1(e, finite_or_zero(x, bad));
+          E::store1(e + 8 * E::kBytes, finite_or_zero(y, bad));
         }
       }
     }
     if (tid == 0 && !a.bump) a.lens_out[unit] = end;
   }
   if (bad) paged_status(a.status, kStatusNonFinite);
+  if (off_table) paged_status(a.status, kStatusBadItem);
 }
 
 // ---- gather ----
@@ -454,11 +505,13 @@ hipError_t launch_norm_rope(const NormArgs& a, hipStream_t s) {
 hipError_t launch_paged_append(const PagedArgs& a, hipStream_t s) {
   const int units = a.c.n_seqs * a.c.n_kv_heads;
   // Blocks that max_new rows can fill from any starting row, at least one workgroup.
-  const int fills = a.max_new > 0 ? (a.max_new + kBlock - 1) / kBlock : 1;
+  const int64_t fills = a.max_new > 0 ? (a.max_new + kBlock - 1) / kBlock : 1;
   PagedArgs x = a;
   // In place, counts read by several workgroups are advanced by a launch of their own.
   x.bump = a.lens_out == a.c.lens && fills > 1;
-  dispatch(a.c, AppendLaunch{x, dim3(fills, units), s});
+  x.append_by8 = fills >= 8;
+  const int64_t ranges = x.append_by8 ? (fills + 7) / 8 * 8 : fills;
+  dispatch(a.c, AppendLaunch{x, dim3(uint32_t(ranges * a.c.n_kv_heads), a.c.n_seqs), s});
   if (x.bump)
     hipLaunchKernelGGL(bump_kernel, dim3((units + 255) / 256), dim3(256), 0, s, x, units);
   return hipGetLastError();

@@ -21,6 +21,7 @@ struct PagedArgs {
   const int32_t* head_new;
   int32_t* lens_out;       // append: where the new counts go (never null)
   int32_t bump;            // append: 1: a second launch advances lens_out == lens
+  int32_t append_by8;      // append: 1: a range's heads are eight workgroups apart
   int32_t page_shift;      // log2(page_blocks)
   uint32_t* status;
   // attention
@@ -91,11 +92,16 @@ template <> struct Elem<false> {
     *static_cast<uint4*>(p) =
         make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
   }
-  static __device__ void load2(const void* p, float& a, float& b) {
-    const uint32_t u = *static_cast<const uint32_t*>(p);
+  using Pair = uint32_t;   // two elements as loaded
+  static __device__ Pair ld_pair(const Buf& b, int off, int uniform) {
+    return __builtin_amdgcn_raw_buffer_load_b32(b.r, off, uniform, 0);
+  }
+  static __device__ void split(Pair u, float& a, float& b) {
     a = __builtin_bit_cast(float, u << 16);
     b = __builtin_bit_cast(float, u & 0xFFFF0000u);
   }
+  static __device__ void load2(const void* p, float& a, float& b) { split(*static_cast<const Pair*>(p), a, b); }
+  static __device__ float load1(const void* p) { return float(*static_cast<const __bf16*>(p)); }
   static __device__ void store2(void* p, float a, float b) {
     *static_cast<uint32_t*>(p) = pack2(a, b);
   }
@@ -116,11 +122,16 @@ template <> struct Elem<true> {
     static_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
     static_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
   }
-  static __device__ void load2(const void* p, float& a, float& b) {
-    const float2 u = *static_cast<const float2*>(p);
+  using Pair = float2;
+  static __device__ Pair ld_pair(const Buf& b, int off, int uniform) {
+    return __builtin_bit_cast(float2, __builtin_amdgcn_raw_buffer_load_b64(b.r, off, uniform, 0));
+  }
+  static __device__ void split(Pair u, float& a, float& b) {
     a = u.x;
     b = u.y;
   }
+  static __device__ void load2(const void* p, float& a, float& b) { split(*static_cast<const Pair*>(p), a, b); }
+  static __device__ float load1(const void* p) { return *static_cast<const float*>(p); }
   static __device__ void store2(void* p, float a, float b) {
     *static_cast<float2*>(p) = make_float2(a, b);
   }

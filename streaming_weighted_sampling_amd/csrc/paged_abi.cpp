@@ -220,11 +220,15 @@ nx_status nx_paged_append(const nx_paged* cache, const nx_rope* rope, const nx_r
   nx_status st = check_cache(cache);
   if (st != NX_OK) return st;
   if (n_rows < 0 || max_new < 0 || max_new > kMaxCacheRows) return NX_EINVAL;
+  // The launch's workgroups are numbered in 31 bits.
+  if ((int64_t(max_new) / kBlock + 8) * cache->n_kv_heads > INT32_MAX) return NX_EUNSUPPORTED;
   if (new_start == nullptr && int64_t(cache->n_seqs) * max_new > n_rows) return NX_EINVAL;
   if ((st = check_rope(rope, cache->head_dim)) != NX_OK) return st;
   const int64_t esz = elem_size(cache->dtype), d = cache->head_dim;
   const RowSet sk{k, n_rows, cache->n_kv_heads, d, esz}, sv{v, n_rows, cache->n_kv_heads, d, esz};
   if ((st = check_rows(sk, false)) != NX_OK || (st = check_rows(sv, false)) != NX_OK) return st;
+  // A block's 32 rows are addressed by 32-bit offsets.
+  if (std::max(k->row_stride, v->row_stride) * esz >= (int64_t(1) << 31) / kBlock - 4096) return NX_EUNSUPPORTED;
   const CacheRanges cr = cache_ranges(cache);
   const int64_t units = int64_t(cache->n_seqs) * cache->n_kv_heads;
   const Range lens = bytes_at(cache->lens, units * 4);
