@@ -25,13 +25,13 @@ struct PagedArgs {
   int32_t page_shift;      // log2(page_blocks)
   uint32_t* status;
   // attention
-  int32_t group, max_q, n_rt, n_wg;   // query-row tiles, shares
-  int32_t min_share;       // fewest blocks of a share
-  int32_t whole;           // 1: a workgroup per head, no shares
+  int32_t group, max_q, n_rt, n_wg;   // query-row tiles, workgroups wanted
+  int32_t min_share;       // fewest blocks of a full piece
+  int32_t whole;           // 1: a workgroup per head, no pieces
   int32_t stream_nt;       // 1: the codes are read past the caches
   float scale_log2;        // scale * log2(e)
   float* lse;
-  int2* pieces;            // [units]: a head's pieces (0: written whole) and its first partial
+  int2* pieces;            // [units]: a head's pieces (0: written at once) and its first partial
   float* part_o;           // [2 * n_wg][n_rt][tile rows][D]
   float* part_ml;          // [2 * n_wg][n_rt][tile rows][2]: (base, sum), log2 units
   // gather

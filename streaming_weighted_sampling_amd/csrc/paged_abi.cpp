@@ -12,14 +12,20 @@ namespace {
 
 constexpr int64_t kMaxCacheRows = int64_t(1) << 24;
 constexpr int64_t kCUs = 256;
-// Resident attention workgroups per CU (registers): 16-row and 32-row tiles.
-constexpr int64_t kResident16 = 1, kResident32 = 2;
-constexpr int64_t kMinShare = 4;        // blocks: one per wavefront
+// Workgroups per CU that an attention call is cut into.  16-row tiles: one
+// where that leaves four pieces a head (it reads at the memory's rate already,
+// with fewer pieces to merge: 8 heads of 32768 rows 19.8 us, two 21.5), else
+// two (128 uneven heads: 66 us, one 75).  32-row tiles: two (registers).
+constexpr int64_t kPiecesPerHead = 4;
+constexpr int64_t kMinShare = 4;        // blocks of a full piece: one per wavefront
 // Heads of up to this many rows are taken whole by a workgroup each (8 heads of
 // 1024 rows: 9.5 us, in shares 9.3; of 819: 9.2 and 12.3), of up to twice as many
 // where there are kManyHeads of them (128 of 2048: 15.8 and 19.3).
 constexpr int64_t kWholeTokens = 1024, kManyHeads = 64;
-constexpr int64_t kStreamBytes = int64_t(256) << 20;
+// Codes of more than this many bytes are read past the caches (a quarter of
+// the 256 MB cache: other layers' calls lie between two reads of the same
+// bytes; 268 MB: 50.8 us, cached 57.2, 134 MB: 30.3 and 33.7).
+constexpr int64_t kStreamBytes = int64_t(64) << 20;
 
 int32_t elem_size(int32_t dtype) { return dtype == NX_BF16 ? 2 : 4; }
 bool aligned(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -128,7 +134,8 @@ PagedArgs base_args(const nx_paged* c) {
   return a;
 }
 
-// How an attention call is cut: query-row tiles and shares of the line of blocks.
+// How an attention call is cut: query-row tiles and pieces of about equal size.
+// Heads in several pieces have at most 2 n_wg pieces together.
 struct Cut {
   int64_t tile, n_rt, n_wg;
   int64_t bytes;         // of codes, at max_tokens rows a head
@@ -141,10 +148,11 @@ nx_status make_cut(const nx_paged* c, int64_t max_tokens, int64_t max_q, Cut* ou
   const int64_t tile = paged_tile_rows(rows);
   const int64_t n_rt = (rows + tile - 1) / tile;
   const int64_t units = int64_t(c->n_seqs) * c->n_kv_heads;
-  // One round of workgroups fills the chip (kResident per CU); no more than
-  // there are smallest shares.
+  // One round of workgroups fills the chip; no more than there are smallest
+  // pieces.
   const int64_t blocks = units * std::max<int64_t>(1, (max_tokens + kBlock - 1) / kBlock);
-  const int64_t most = std::max<int64_t>(8, kCUs * (tile == 16 ? kResident16 : kResident32) / n_rt);
+  const int64_t per_cu = tile == 16 && units * kPiecesPerHead <= kCUs ? 1 : 2;
+  const int64_t most = std::max<int64_t>(8, kCUs * per_cu / n_rt);
   const int64_t n_wg = std::min(most, (blocks + kMinShare - 1) / kMinShare);
   *out = {tile, n_rt, (n_wg + 7) / 8 * 8, blocks * kBlock * 2 * c->head_dim,
           max_tokens <= (units >= kManyHeads ? 2 * kWholeTokens : kWholeTokens)};

@@ -3,13 +3,15 @@
 //   o_r = sum_t p_rt v_t / sum_t p_rt,   p_rt = exp(scale q_r . k_t - m_r)
 //
 // One pass over the cached rows with a running reference m_r and sum per query
-// row.  The blocks of all (sequence, KV head)s form one line that is cut into
-// equal shares, one per workgroup, whatever the heads' lengths: every CU gets
-// the same bytes, in one round.  A share covers pieces of one or several
-// heads; the four wavefronts split a piece and merge through LDS.  A head that
-// lies in one share is written at once, otherwise its pieces leave partials
-// (m, sum, o) and the last workgroup to arrive merges them in head order, so
-// the result does not depend on the order of arrival.
+// row.  The call's blocks, all (sequence, KV head)s together, are cut into
+// pieces of about equal size, one per workgroup, whatever the heads' lengths:
+// a head of n blocks gives ceil(n / share) pieces, share = all blocks over the
+// number of workgroups wanted.  The wavefronts split a piece and merge through
+// LDS.  A head in one piece is written at once, otherwise its pieces leave
+// partials (base, sum, o) that a second small kernel merges in head order.
+// (Merging by the last workgroup to arrive at a counter instead cost 4 us in
+// the counter's atomics alone at 54 pieces a head, all arriving at once; cuts
+// that run on from one head into the next cost a workgroup a second start.)
 //
 // Matrix form, per block of 32 rows: S^T = K Q^T and O^T += V^T P^T with
 // 16x16x32 f16 MFMAs.  8-bit codes are exact in f16, so the codes are the
@@ -94,54 +96,86 @@ __device__ inline int wave_scan(int x) {
   return x;
 }
 
-// This workgroup's share [begin, end) of the line and the head it starts in.
-struct Share {
-  int size, begin, end;
-  int unit;            // first head with blocks in the share
-  int unit_at;         // where that head starts in the line
+// One workgroup's piece: blocks [b0, b1) of a head.
+struct Piece {
+  int unit, b0, b1;    // unit < 0: no piece
+  int nth, of;         // which of the head's pieces
+  int slot;            // partial of the head's first piece (heads in several pieces only)
 };
 
-// Every wavefront sums the heads' weights for itself, 64 heads at a time: no
-// barrier, and the sums of all workgroups are the same.
-__device__ inline Share find_share(const PagedArgs& a, int wg, int units, int lane) {
+// Every wavefront works the cut out for itself (no barrier; the same in all
+// workgroups).  The share is the smallest that cuts the heads into at most
+// n_wg pieces: one more would be a second round on some CU, and a second
+// round of a piece costs as much as the first (16 heads of about 4096 blocks
+// on 256 CUs: 137 us with 265 pieces, 93 with 256).
+constexpr int kHeadRegs = 4;   // heads whose weights stay in registers, times 64
+__device__ inline Piece find_piece(const PagedArgs& a, int wg, int units, int lane) {
   auto weight = [&](int unit) {
     if (unit >= units) return 0;
     const Job j = make_job(a, unit);
     if (!j.ok && wg == 0) paged_status(a.status, kStatusBadItem);
     return j.n_blk;
   };
-  Share s;
+  int w[kHeadRegs];
   int64_t total = 0;
-  int mine = 0, incl = 0;
-  for (int u0 = 0; u0 < units; u0 += 64) {
-    mine = weight(u0 + lane);
-    incl = wave_scan(mine);
-    total += __builtin_amdgcn_readlane(incl, 63);
+#pragma unroll
+  for (int x = 0; x < kHeadRegs; ++x) {
+    w[x] = 0;
+    if (64 * x < units) {
+      w[x] = weight(64 * x + lane);
+      total += __builtin_amdgcn_readlane(wave_scan(w[x]), 63);
+    }
   }
+  for (int u0 = 64 * kHeadRegs; u0 < units; u0 += 64)
+    total += __builtin_amdgcn_readlane(wave_scan(weight(u0 + lane)), 63);
+  Piece p{-1, 0, 0, 0, 0, 0};
   if (total > INT32_MAX) {   // more blocks than a pool can hold many times over
     if (wg == 0) paged_status(a.status, kStatusBadItem);
-    total = 0;
+    return p;
   }
-  s.size = max(a.min_share, int((uint32_t(total) + uint32_t(a.n_wg) - 1) / uint32_t(a.n_wg)));
-  const int64_t begin = int64_t(wg) * s.size;
-  s.begin = int(min(begin, total));
-  s.end = int(min(begin + s.size, total));
-  s.unit = s.unit_at = 0;
-  for (int u0 = 0, at = 0; s.begin < s.end && u0 < units; u0 += 64) {
-    if (units > 64) {
-      mine = weight(u0 + lane);
-      incl = wave_scan(mine);
+  int share = max(a.min_share, int((uint32_t(total) + uint32_t(a.n_wg) - 1) / uint32_t(a.n_wg)));
+  if (units <= 64 * kHeadRegs && 2 * units <= a.n_wg) {
+    // Between total / n_wg and total / (n_wg - units), to within 1/32.
+    int lo = share, hi = max(share, int((uint32_t(total) + uint32_t(a.n_wg - units) - 1) / uint32_t(a.n_wg - units)));
+    while (true) {
+      int n = 0;
+#pragma unroll
+      for (int x = 0; x < kHeadRegs; ++x)
+        if (64 * x < units) n += __builtin_amdgcn_readlane(wave_scan((w[x] + share - 1) / share), 63);
+      if (n <= a.n_wg) hi = share;
+      else lo = share + 1;
+      if (lo >= hi || (hi - lo) * 32 <= hi) break;
+      share = (lo + hi) / 2;
     }
-    const uint64_t hit = __ballot(mine > 0 && at + incl - mine <= s.begin && s.begin < at + incl);
+    share = hi;
+  }
+  for (int u0 = 0, at = 0, slot = 0; u0 < units; u0 += 64) {
+    int mine = 0;
+    if (u0 >= 64 * kHeadRegs) {
+      mine = weight(u0 + lane);
+    } else {
+#pragma unroll
+      for (int x = 0; x < kHeadRegs; ++x)
+        if (u0 == 64 * x) mine = w[x];
+    }
+    const int n = (mine + share - 1) / share, parts = n > 1 ? n : 0;
+    const int n_incl = wave_scan(n), parts_incl = wave_scan(parts);
+    const uint64_t hit = __ballot(at + n_incl - n <= wg && wg < at + n_incl);
     if (hit != 0) {
       const int i = __builtin_ctzll(hit);
-      s.unit = u0 + i;
-      s.unit_at = at + __builtin_amdgcn_readlane(incl - mine, i);
-      break;
+      const int blocks = __builtin_amdgcn_readlane(mine, i);
+      p.unit = u0 + i;
+      p.of = __builtin_amdgcn_readlane(n, i);
+      p.nth = wg - (at + __builtin_amdgcn_readlane(n_incl - n, i));
+      p.slot = slot + __builtin_amdgcn_readlane(parts_incl - parts, i);
+      p.b0 = int(int64_t(blocks) * p.nth / p.of);
+      p.b1 = int(int64_t(blocks) * (p.nth + 1) / p.of);
+      return p;
     }
-    at += __builtin_amdgcn_readlane(incl, 63);
+    at += __builtin_amdgcn_readlane(n_incl, 63);
+    slot += __builtin_amdgcn_readlane(parts_incl, 63);
   }
-  return s;
+  return p;
 }
 
 // Accumulators of a wavefront: query row c of tile rt in lanes (., c).
@@ -237,16 +271,9 @@ __device__ inline void write_lse(const PagedArgs& a, const Job& job, int h, int 
       l == 0.f ? -__builtin_inff() : 0.69314718056f * (log2f(l) - base);
 }
 
-// Partial of share `wg` for the head that starts at unit_at: a share holds at
-// most two, one for a head that covers its start and one for a head that
-// begins inside it and goes on past its end.
-__device__ inline int64_t part_slot(const Share& share, int unit_at, int wg) {
-  return 2 * int64_t(wg) + (unit_at > int64_t(wg) * share.size ? 1 : 0);
-}
-
 // 16 RT query rows a workgroup.  kWhole: workgroup (u, row tile) takes head u
 // whole, for calls of short heads, which then need neither the search for the
-// share nor the merge launch.
+// piece nor the merge launch.
 template <int D, bool kF32, int kFmt, int RT, bool kNT, bool kWhole, int kWaves>
 __global__ __launch_bounds__(64 * kWaves) void attn_kernel(PagedArgs a) {
   using E = Elem<kF32>;
@@ -260,362 +287,343 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(PagedArgs a) {
   __shared__ float sb[kWaves][kRows], sl[kWaves][kRows];
   __shared__ f32x4_t so[kWaves][RT * (D / 16)][64];
 
-  // Workgroups of one share and all its row tiles sit on one XCD (ids eight
-  // apart) and near in time, so that the tiles share its L2.
+  // The row tiles of one piece sit on one XCD (ids eight apart) and near in
+  // time, so that they share its L2.
   const int per8 = 8 * a.n_rt;
   const int wg = !kWhole ? int(blockIdx.x) / per8 * 8 + int(blockIdx.x) % 8 : 0;
   const int rt0 = !kWhole ? int(blockIdx.x) % per8 / 8 : int(blockIdx.x) % a.n_rt;
   const int row0 = rt0 * kRows;
-  Share share;
-  if constexpr (!kWhole) {
-    share = find_share(a, wg, units, threadIdx.x & 63);
-  } else {
-    share.begin = share.unit_at = 0;
-    share.unit = int(blockIdx.x) / a.n_rt;
-    const Job job = make_job(a, share.unit);
+  Piece piece;
+  if constexpr (kWhole) piece = Piece{int(blockIdx.x) / a.n_rt, 0, 0, 0, 1, 0};
+  else piece = find_piece(a, wg, units, threadIdx.x & 63);
+  if (piece.unit < 0) return;
+  const int unit = piece.unit;
+  const Job job = make_job(a, unit);
+  if constexpr (kWhole) {
     if (!job.ok && rt0 == 0 && threadIdx.x == 0) paged_status(a.status, kStatusBadItem);
-    share.size = max(1, job.n_blk);
-    share.end = job.n_blk;
+    piece.b1 = job.n_blk;
   }
-  int at = share.unit_at;
-  int unit = share.unit;
-  for (int pos = share.begin; pos < share.end; ++unit) {
-    const Job job = make_job(a, unit);
-    const int unit_at = at;
-    at += job.n_blk;
-    const int b0 = pos - unit_at;
-    const int b1 = min(job.n_blk, share.end - unit_at);
-    if (job.n_blk == 0) continue;
-    pos = unit_at + b1;
-    if (row0 >= job.rows) continue;
-    const int h = unit % a.c.n_kv_heads;
-    // The lane is opaque in every piece: what depends on it alone is computed
-    // again (a few instructions) and not kept in registers over the loop.
-    int lane = threadIdx.x & 63;
-    asm volatile("" : "+v"(lane));
-    const int c16 = lane & 15, g = lane >> 4;
+  if (row0 >= job.rows) return;
+  const int h = unit % a.c.n_kv_heads, b0 = piece.b0, b1 = piece.b1;
+  const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
 
-    State<D, RT> st;
-    st.vref = 0.f;
-    st.lvref = kNoScale;
-    // Row r sees tokens up to seen[rt]; blocks past all_see need the test.
-    int seen[RT];
+  State<D, RT> st;
+  st.vref = 0.f;
+  st.lvref = kNoScale;
+  // Row r sees tokens up to seen[rt]; blocks past all_see need the test.
+  int seen[RT];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      st.base[rt] = kNoBase;
-      st.l[rt] = 0.f;
+  for (int rt = 0; rt < RT; ++rt) {
+    st.base[rt] = kNoBase;
+    st.l[rt] = 0.f;
 #pragma unroll
-      for (int n = 0; n < D / 16; ++n) st.o[rt][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      seen[rt] = job.len - job.n_q + (row0 + rt * 16 + c16) / a.group;
-    }
-    const int all_see = job.len - job.n_q;
-    const int full = job.len / kBlock;
-    const int per = (b1 - b0 + kWaves - 1) / kWaves;
-    const int w0 = b0 + wave * per, w1 = min(w0 + per, b1), wf = min(w1, full);
-    // Lane j looks up block x0 + j of up to 64 blocks.
-    int slot_l, n8;
-    float ks_l, vs_l;
-    auto look_up = [&](int x0) {
-      n8 = min(wf - x0, 64);
-      slot_l = 0;
-      ks_l = vs_l = 0.f;
-      if (lane < n8) {
-        const int b = x0 + lane;
-        int page = a.c.table[int64_t(unit) * a.c.max_pages + (b >> a.page_shift)];
-        if (page < 0 || page >= a.c.n_pages) {
-          paged_status(a.status, kStatusBadItem);
-          page = 0;
-        }
-        slot_l = (page << a.page_shift) + (b & slot_mask);
-        ks_l = a.c.k_scale[slot_l];
-        vs_l = a.c.v_scale[slot_l];
+    for (int n = 0; n < D / 16; ++n) st.o[rt][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    seen[rt] = job.len - job.n_q + (row0 + rt * 16 + c16) / a.group;
+  }
+  const int all_see = job.len - job.n_q;
+  const int full = job.len / kBlock;
+  const int per = (b1 - b0 + kWaves - 1) / kWaves;
+  const int w0 = b0 + wave * per, w1 = min(w0 + per, b1), wf = min(w1, full);
+  // Lane j looks up block x0 + j of up to 64 blocks.
+  int slot_l, n8;
+  float ks_l, vs_l;
+  auto look_up = [&](int x0) {
+    n8 = min(wf - x0, 64);
+    slot_l = 0;
+    ks_l = vs_l = 0.f;
+    if (lane < n8) {
+      const int b = x0 + lane;
+      int page = a.c.table[int64_t(unit) * a.c.max_pages + (b >> a.page_shift)];
+      if (page < 0 || page >= a.c.n_pages) {
+        paged_status(a.status, kStatusBadItem);
+        page = 0;
       }
-    };
-    // A block's K is fetched while the block before is settled, its V while
-    // its own logits form: each register is refilled as soon as it is used.
-    uint4 kr[kKL], vr[kVL];
-    auto codes = [&](const void* base, int i) {
-      const int64_t at = int64_t(__builtin_amdgcn_readlane(slot_l, i)) * (kBlock * D);
-      return Buf(static_cast<const char*>(base) + at, kBlock * D);
-    };
-    auto load_k = [&](int i) {
-      const Buf kb = codes(a.c.k_codes, i);
+      slot_l = (page << a.page_shift) + (b & slot_mask);
+      ks_l = a.c.k_scale[slot_l];
+      vs_l = a.c.v_scale[slot_l];
+    }
+  };
+  // A block's K is fetched while the block before is settled, its V while
+  // its own logits form: each register is refilled as soon as it is used.
+  uint4 kr[kKL], vr[kVL];
+  auto codes = [&](const void* base, int i) {
+    const int64_t at = int64_t(__builtin_amdgcn_readlane(slot_l, i)) * (kBlock * D);
+    return Buf(static_cast<const char*>(base) + at, kBlock * D);
+  };
+  auto load_k = [&](int i) {
+    const Buf kb = codes(a.c.k_codes, i);
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x)
-          kr[u * (D / 64) + x] =
-              kb.ld16<kNT ? kNonTemporal : 0>(((c16 / 4) * 8 + c16 % 4) * D + 16 * g + u * 4 * D + 64 * x);
-    };
-    auto load_v = [&](int i) {
-      const Buf vb = codes(a.c.v_codes, i);
+      for (int x = 0; x < D / 64; ++x)
+        kr[u * (D / 64) + x] =
+            kb.ld16<kNT ? kNonTemporal : 0>(((c16 / 4) * 8 + c16 % 4) * D + 16 * g + u * 4 * D + 64 * x);
+  };
+  auto load_v = [&](int i) {
+    const Buf vb = codes(a.c.v_codes, i);
 #pragma unroll
-      for (int n = 0; n < kVL; ++n) vr[n] = vb.ld16<kNT ? kNonTemporal : 0>((g * D + 2 * c16) * 8 + 256 * n);
-    };
-    // The first block is on its way while q is prepared.
-    if (w0 < wf) {
-      look_up(w0);
+    for (int n = 0; n < kVL; ++n) vr[n] = vb.ld16<kNT ? kNonTemporal : 0>((g * D + 2 * c16) * 8 + 256 * n);
+  };
+  // The first block is on its way while q is prepared.
+  if (w0 < wf) {
+    look_up(w0);
+    load_k(0);
+    load_v(0);
+  }
+
+  // ---- q: f16 operand terms and the factor of the logits per row ----
+  h8_t q[RT][kC][NP];
+  float qmul[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int r = row0 + rt * 16 + c16;
+    const char* src = static_cast<const char*>(a.q.p) + row_offset<kF32>(a, a.q, job, h, min(r, job.rows - 1));
+    float x[kC][8];
+    float top = 0.f;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      E::load8(src + (64 * (c / 2) + 16 * g + 8 * (c % 2)) * E::kBytes, x[c]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (r >= job.rows) x[c][e] = 0.f;
+        top = fmaxf(top, fabsf(x[c][e]));
+      }
+    }
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    const int ex = top > 0.f ? int(__builtin_bit_cast(uint32_t, top) >> 23) - 127 : 0;
+#pragma unroll
+    for (int c = 0; c < kC; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float s = ldexpf(x[c][e], 13 - ex);
+        const _Float16 hi = _Float16(s);
+        q[rt][c][0][e] = hi;
+        if constexpr (kF32) q[rt][c][NP - 1][e] = _Float16(s - float(hi));
+      }
+    qmul[rt] = ldexpf(a.scale_log2, ex - 13);
+  }
+
+  for (int x0 = w0; x0 < wf; x0 += 64) {
+    if (x0 > w0) {
+      look_up(x0);
       load_k(0);
       load_v(0);
     }
-
-    // ---- q: f16 operand terms and the factor of the logits per row ----
-    h8_t q[RT][kC][NP];
-    float qmul[RT];
+    const float lvs_l = vs_l > 0.f ? log2f(vs_l) : kNoScale * 4.f;
+    f32x4_t s[RT][2];
+    auto products = [&] {   // s = K q^T of the block in kr
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int r = row0 + rt * 16 + c16;
-      const char* src = static_cast<const char*>(a.q.p) + row_offset<kF32>(a, a.q, job, h, min(r, job.rows - 1));
-      float x[kC][8];
-      float top = 0.f;
+      for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        E::load8(src + (64 * (c / 2) + 16 * g + 8 * (c % 2)) * E::kBytes, x[c]);
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (r >= job.rows) x[c][e] = 0.f;
-          top = fmaxf(top, fabsf(x[c][e]));
-        }
-      }
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const int ex = top > 0.f ? int(__builtin_bit_cast(uint32_t, top) >> 23) - 127 : 0;
-#pragma unroll
-      for (int c = 0; c < kC; ++c)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float s = ldexpf(x[c][e], 13 - ex);
-          const _Float16 hi = _Float16(s);
-          q[rt][c][0][e] = hi;
-          if constexpr (kF32) q[rt][c][NP - 1][e] = _Float16(s - float(hi));
-        }
-      qmul[rt] = ldexpf(a.scale_log2, ex - 13);
-    }
-
-    for (int x0 = w0; x0 < wf; x0 += 64) {
-      if (x0 > w0) {
-        look_up(x0);
-        load_k(0);
-        load_v(0);
-      }
-      const float lvs_l = vs_l > 0.f ? log2f(vs_l) : kNoScale * 4.f;
-      f32x4_t s[RT][2];
-      auto products = [&] {   // s = K q^T of the block in kr
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int c = 0; c < kC; ++c) {
-            const uint4 w = kr[u * (D / 64) + c / 2];
-            const h8_t k8 = c % 2 ? codes_f16<kFmt>(w.z, w.w) : codes_f16<kFmt>(w.x, w.y);
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-              for (int np = 0; np < NP; ++np)
-                s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, q[rt][c][np], s[rt][u], 0, 0, 0);
-          }
-      };
-      for (int i = 0; i < n8; ++i) {
-        products();
-        if (i + 1 < n8) load_k(i + 1);
-        const float ks = lane_of(ks_l, i), vs = lane_of(vs_l, i), lvs = lane_of(lvs_l, i);
-        float t[RT], z[RT][8];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) t[rt] = fmaxf(ks * qmul[rt], 0x1p-126f);   // > 0: hidden stays -infinity
-        const int t0 = (x0 + i) * kBlock;
-        if (t0 + kBlock - 1 > all_see) {
+        for (int c = 0; c < kC; ++c) {
+          const uint4 w = kr[u * (D / 64) + c / 2];
+          const h8_t k8 = c % 2 ? codes_f16<kFmt>(w.z, w.w) : codes_f16<kFmt>(w.x, w.y);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (t0 + 8 * g + e > seen[rt]) s[rt][e / 4][e % 4] = -__builtin_inff();
+            for (int np = 0; np < NP; ++np)
+              s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, q[rt][c][np], s[rt][u], 0, 0, 0);
         }
-        const float back = exponents<D, RT>(st, s, t, vs, lvs, kLeast, z);
-        exponentiate<D, RT>(st, back, z);
-        h8_t pp[RT][NP];
+    };
+    for (int i = 0; i < n8; ++i) {
+      products();
+      if (i + 1 < n8) load_k(i + 1);
+      const float ks = lane_of(ks_l, i), vs = lane_of(vs_l, i), lvs = lane_of(lvs_l, i);
+      float t[RT], z[RT][8];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) t[rt] = fmaxf(ks * qmul[rt], 0x1p-126f);   // > 0: hidden stays -infinity
+      const int t0 = (x0 + i) * kBlock;
+      if (t0 + kBlock - 1 > all_see) {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const _Float16 hi = _Float16(z[rt][e]);
-            pp[rt][0][e] = hi;
-            if constexpr (kF32) pp[rt][NP - 1][e] = _Float16(z[rt][e] - float(hi));
-          }
-#pragma unroll
-        for (int n = 0; n < kVL; ++n)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const h8_t v8 = u ? codes_f16<kFmt>(vr[n].z, vr[n].w) : codes_f16<kFmt>(vr[n].x, vr[n].y);
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-              for (int np = 0; np < NP; ++np)
-                st.o[rt][2 * n + u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, pp[rt][np],
-                                                                           st.o[rt][2 * n + u], 0, 0, 0);
-          }
-        if (i + 1 < n8) load_v(i + 1);
+          for (int e = 0; e < 8; ++e)
+            if (t0 + 8 * g + e > seen[rt]) s[rt][e / 4][e % 4] = -__builtin_inff();
       }
-    }
-    if (w0 <= full && full < w1 && full * kBlock < job.len) {
-      // The tail: up to 31 rows in the call's own type.  bf16 rows use bf16
-      // MFMAs (q as it is, p in two terms), fp32 rows fp32 MFMAs.
-      const int nt = job.len - full * kBlock;
-      const int64_t tail_at = int64_t(unit) * kBlock * D * E::kBytes;
-      const Buf kt(static_cast<const char*>(a.c.k_tail) + tail_at, kBlock * D * E::kBytes);
-      const Buf vt(static_cast<const char*>(a.c.v_tail) + tail_at, kBlock * D * E::kBytes);
-      const int k_at = ((c16 / 4) * 8 + c16 % 4) * D * E::kBytes;
-      const int v_at = (g * D + 2 * c16) * 8 * E::kBytes;
-      f32x4_t s[RT][2];
-      float t[RT];
+      const float back = exponents<D, RT>(st, s, t, vs, lvs, kLeast, z);
+      exponentiate<D, RT>(st, back, z);
+      h8_t pp[RT][NP];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        s[rt][0] = s[rt][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        t[rt] = fmaxf(a.scale_log2, 0x1p-126f);
-        const int r = row0 + rt * 16 + c16;   // rows past the last repeat it; they are not written
-        const char* src = static_cast<const char*>(a.q.p) + row_offset<kF32>(a, a.q, job, h, min(r, job.rows - 1));
-        if constexpr (!kF32) {
+      for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-          for (int c = 0; c < kC; ++c) {
-            const int d = 64 * (c / 2) + 16 * g + 8 * (c % 2);
-            const uint4 qw = *reinterpret_cast<const uint4*>(src + d * 2);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const uint4 kw = kt.ld16(k_at + u * 4 * D * 2 + d * 2);
-              s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  __builtin_bit_cast(bf16x8_t, kw), __builtin_bit_cast(bf16x8_t, qw), s[rt][u], 0, 0, 0);
-            }
-          }
-        } else {
-          for (int c = 0; c < D / 16; ++c) {
-            const int d = 16 * c + 4 * g;
-            const float4 qw = *reinterpret_cast<const float4*>(src + d * 4);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const float4 kw = __builtin_bit_cast(float4, kt.ld16(k_at + u * 4 * D * 4 + d * 4));
-              s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x4f32(kw.x, qw.x, s[rt][u], 0, 0, 0);
-              s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x4f32(kw.y, qw.y, s[rt][u], 0, 0, 0);
-              s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x4f32(kw.z, qw.z, s[rt][u], 0, 0, 0);
-              s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x4f32(kw.w, qw.w, s[rt][u], 0, 0, 0);
-            }
-          }
+        for (int e = 0; e < 8; ++e) {
+          const _Float16 hi = _Float16(z[rt][e]);
+          pp[rt][0][e] = hi;
+          if constexpr (kF32) pp[rt][NP - 1][e] = _Float16(z[rt][e] - float(hi));
         }
-        // Rows past the tail's count may hold anything.
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (8 * g + e >= nt || full * kBlock + 8 * g + e > seen[rt]) s[rt][e / 4][e % 4] = -__builtin_inff();
-      }
-      float p[RT][8];
-      exponentiate<D, RT>(st, exponents<D, RT>(st, s, t, 1.f, 0.f, kLeastTail, p), p);
-#pragma unroll
-      for (int n = 0; n < D / 32; ++n)
+      for (int n = 0; n < kVL; ++n)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          // Zeros where no row is: whatever lies there must not meet p = 0.
-          float v[8];
-          const int at = v_at + (32 * n + u) * 8 * E::kBytes;
-          E::unpack8(vt.ld16(at), kF32 ? vt.ld16(at + 16) : uint4{}, v);
+          const h8_t v8 = u ? codes_f16<kFmt>(vr[n].z, vr[n].w) : codes_f16<kFmt>(vr[n].x, vr[n].y);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = 8 * g + e < nt ? v[e] : 0.f;
+          for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            if constexpr (!kF32) {
-              bf16x8_t v8, hi, lo;
+            for (int np = 0; np < NP; ++np)
+              st.o[rt][2 * n + u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, pp[rt][np],
+                                                                         st.o[rt][2 * n + u], 0, 0, 0);
+        }
+      if (i + 1 < n8) load_v(i + 1);
+    }
+  }
+  if (w0 <= full && full < w1 && full * kBlock < job.len) {
+    // The tail: up to 31 rows in the call's own type.  bf16 rows use bf16
+    // MFMAs (q as it is, p in two terms), fp32 rows fp32 MFMAs.
+    const int nt = job.len - full * kBlock;
+    const int64_t tail_at = int64_t(unit) * kBlock * D * E::kBytes;
+    const Buf kt(static_cast<const char*>(a.c.k_tail) + tail_at, kBlock * D * E::kBytes);
+    const Buf vt(static_cast<const char*>(a.c.v_tail) + tail_at, kBlock * D * E::kBytes);
+    const int k_at = ((c16 / 4) * 8 + c16 % 4) * D * E::kBytes;
+    const int v_at = (g * D + 2 * c16) * 8 * E::kBytes;
+    f32x4_t s[RT][2];
+    float t[RT];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float x = p[rt][e];
-                v8[e] = __bf16(v[e]);
-                hi[e] = __bf16(x);
-                lo[e] = __bf16(x - float(hi[e]));
-              }
-              st.o[rt][2 * n + u] =
-                  __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8, hi, st.o[rt][2 * n + u], 0, 0, 0);
-              st.o[rt][2 * n + u] =
-                  __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8, lo, st.o[rt][2 * n + u], 0, 0, 0);
-            } else {
+    for (int rt = 0; rt < RT; ++rt) {
+      s[rt][0] = s[rt][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      t[rt] = fmaxf(a.scale_log2, 0x1p-126f);
+      const int r = row0 + rt * 16 + c16;   // rows past the last repeat it; they are not written
+      const char* src = static_cast<const char*>(a.q.p) + row_offset<kF32>(a, a.q, job, h, min(r, job.rows - 1));
+      if constexpr (!kF32) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                st.o[rt][2 * n + u] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                    v[e], p[rt][e], st.o[rt][2 * n + u], 0, 0, 0);
-            }
+        for (int c = 0; c < kC; ++c) {
+          const int d = 64 * (c / 2) + 16 * g + 8 * (c % 2);
+          const uint4 qw = *reinterpret_cast<const uint4*>(src + d * 2);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint4 kw = kt.ld16(k_at + u * 4 * D * 2 + d * 2);
+            s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8_t, kw), __builtin_bit_cast(bf16x8_t, qw), s[rt][u], 0, 0, 0);
           }
         }
-    }
-
-    // ---- merge the wavefronts ----
+      } else {
+        for (int c = 0; c < D / 16; ++c) {
+          const int d = 16 * c + 4 * g;
+          const float4 qw = *reinterpret_cast<const float4*>(src + d * 4);
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      st.l[rt] += __shfl_xor(st.l[rt], 16, 64);
-      st.l[rt] += __shfl_xor(st.l[rt], 32, 64);
-      if (g == 0) {
-        sb[wave][rt * 16 + c16] = st.base[rt];
-        sl[wave][rt * 16 + c16] = st.l[rt];
+          for (int u = 0; u < 2; ++u) {
+            const float4 kw = __builtin_bit_cast(float4, kt.ld16(k_at + u * 4 * D * 4 + d * 4));
+            s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x4f32(kw.x, qw.x, s[rt][u], 0, 0, 0);
+            s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x4f32(kw.y, qw.y, s[rt][u], 0, 0, 0);
+            s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x4f32(kw.z, qw.z, s[rt][u], 0, 0, 0);
+            s[rt][u] = __builtin_amdgcn_mfma_f32_16x16x4f32(kw.w, qw.w, s[rt][u], 0, 0, 0);
+          }
+        }
       }
+      // Rows past the tail's count may hold anything.
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (8 * g + e >= nt || full * kBlock + 8 * g + e > seen[rt]) s[rt][e / 4][e % 4] = -__builtin_inff();
     }
-    __syncthreads();
+    float p[RT][8];
+    exponentiate<D, RT>(st, exponents<D, RT>(st, s, t, 1.f, 0.f, kLeastTail, p), p);
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int r = rt * 16 + c16;
-      float bmin = sb[0][r];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) bmin = fminf(bmin, sb[w][r]);
-      const float f = exp2f(bmin - st.base[rt]) * st.vref;
-#pragma unroll
-      for (int n = 0; n < D / 16; ++n) st.o[rt][n] *= f;
-    }
-    // Each wavefront leaves its o in LDS and sums its part of the columns.
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int n = 0; n < D / 16; ++n) so[wave][rt * (D / 16) + n][lane] = st.o[rt][n];
-    __syncthreads();
-
-    // ---- the result, or a partial ----
-    const int first = unit_at / share.size, last = (unit_at + job.n_blk - 1) / share.size;
-    constexpr int kParts = RT * (D / 32);      // (row tile, 32 columns) pairs
-#pragma unroll
-    for (int k = 0; k < (kParts + kWaves - 1) / kWaves; ++k) {
-      const int part = k * kWaves + wave;
-      if (kParts % kWaves != 0 && part >= kParts) break;
-      const int rt = part / (D / 32), n = part % (D / 32);
-      float x[8];
+    for (int n = 0; n < D / 32; ++n)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        f32x4_t o = so[0][2 * part + u][lane];
+        // Zeros where no row is: whatever lies there must not meet p = 0.
+        float v[8];
+        const int at = v_at + (32 * n + u) * 8 * E::kBytes;
+        E::unpack8(vt.ld16(at), kF32 ? vt.ld16(at + 16) : uint4{}, v);
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) o += so[w][2 * part + u][lane];
+        for (int e = 0; e < 8; ++e) v[e] = 8 * g + e < nt ? v[e] : 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[2 * e + u] = o[e];
+        for (int rt = 0; rt < RT; ++rt) {
+          if constexpr (!kF32) {
+            bf16x8_t v8, hi, lo;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float x = p[rt][e];
+              v8[e] = __bf16(v[e]);
+              hi[e] = __bf16(x);
+              lo[e] = __bf16(x - float(hi[e]));
+            }
+            st.o[rt][2 * n + u] =
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8, hi, st.o[rt][2 * n + u], 0, 0, 0);
+            st.o[rt][2 * n + u] =
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8, lo, st.o[rt][2 * n + u], 0, 0, 0);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              st.o[rt][2 * n + u] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                  v[e], p[rt][e], st.o[rt][2 * n + u], 0, 0, 0);
+          }
+        }
       }
-      const int r = row0 + rt * 16 + c16;
-      if (r >= job.rows) continue;
-      const int rr = rt * 16 + c16;
-      float bmin = sb[0][rr];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) bmin = fminf(bmin, sb[w][rr]);
-      float l = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) l += sl[w][rr] * exp2f(bmin - sb[w][rr]);
-      if (first == last) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= inv;
-        E::store8(static_cast<char*>(a.out.p) + row_offset<kF32>(a, a.out, job, h, r) +
-                      (32 * n + 8 * g) * E::kBytes, x);
-        if (a.lse != nullptr && g == 0 && n == 0) write_lse(a, job, h, r, l, bmin);
-      } else {
-        const int64_t pr = (part_slot(share, unit_at, wg) * a.n_rt + rt0) * kRows + rr;
-        Elem<true>::store8(a.part_o + pr * D + 32 * n + 8 * g, x);
-        if (g == 0 && n == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * pr) = make_float2(bmin, l);
-      }
-    }
-    // The head's first piece says where its pieces are, in the first row
-    // tile's name (the cut is the same for all).
-    if (!kWhole && b0 == 0 && rt0 == 0 && threadIdx.x == 0)
-      a.pieces[unit] = first == last ? make_int2(0, 0)
-                                     : make_int2(last - first + 1, int(part_slot(share, unit_at, first)));
-    __syncthreads();   // LDS is reused by the next piece
   }
+
+  // ---- merge the wavefronts ----
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    st.l[rt] += __shfl_xor(st.l[rt], 16, 64);
+    st.l[rt] += __shfl_xor(st.l[rt], 32, 64);
+    if (g == 0) {
+      sb[wave][rt * 16 + c16] = st.base[rt];
+      sl[wave][rt * 16 + c16] = st.l[rt];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int r = rt * 16 + c16;
+    float bmin = sb[0][r];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) bmin = fminf(bmin, sb[w][r]);
+    const float f = exp2f(bmin - st.base[rt]) * st.vref;
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) st.o[rt][n] *= f;
+  }
+  // Each wavefront leaves its o in LDS and sums its part of the columns.
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) so[wave][rt * (D / 16) + n][lane] = st.o[rt][n];
+  __syncthreads();
+
+  // ---- the result, or a partial ----
+  constexpr int kParts = RT * (D / 32);      // (row tile, 32 columns) pairs
+#pragma unroll
+  for (int k = 0; k < (kParts + kWaves - 1) / kWaves; ++k) {
+    const int part = k * kWaves + wave;
+    if (kParts % kWaves != 0 && part >= kParts) break;
+    const int rt = part / (D / 32), n = part % (D / 32);
+    float x[8];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      f32x4_t o = so[0][2 * part + u][lane];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) o += so[w][2 * part + u][lane];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[2 * e + u] = o[e];
+    }
+    const int r = row0 + rt * 16 + c16;
+    if (r >= job.rows) continue;
+    const int rr = rt * 16 + c16;
+    float bmin = sb[0][rr];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) bmin = fminf(bmin, sb[w][rr]);
+    float l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) l += sl[w][rr] * exp2f(bmin - sb[w][rr]);
+    if (piece.of == 1) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= inv;
+      E::store8(static_cast<char*>(a.out.p) + row_offset<kF32>(a, a.out, job, h, r) +
+                    (32 * n + 8 * g) * E::kBytes, x);
+      if (a.lse != nullptr && g == 0 && n == 0) write_lse(a, job, h, r, l, bmin);
+    } else {
+      const int64_t pr = (int64_t(piece.slot + piece.nth) * a.n_rt + rt0) * kRows + rr;
+      Elem<true>::store8(a.part_o + pr * D + 32 * n + 8 * g, x);
+      if (g == 0 && n == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * pr) = make_float2(bmin, l);
+    }
+  }
+  // The head's first piece says where its pieces are, in the first row
+  // tile's name (the cut is the same for all).
+  if (!kWhole && piece.nth == 0 && rt0 == 0 && threadIdx.x == 0)
+    a.pieces[unit] = make_int2(piece.of > 1 ? piece.of : 0, piece.slot);
 }
 
 // Merges the pieces of one query row of one head, in order: D / 4 lanes a
@@ -628,13 +636,11 @@ __global__ __launch_bounds__(256) void attn_merge_kernel(PagedArgs a, int tile) 
   const int2 pieces = a.pieces[unit];   // (count, slot of the first); not written without queries
   const Job job = make_job(a, unit);
   if (r >= job.rows || pieces.x == 0) return;
+  // (Not a cut of this call: it had too many blocks and wrote none.)
+  if (pieces.x < 0 || pieces.y < 0 || int64_t(pieces.x) + pieces.y > 2 * int64_t(a.n_wg)) return;
   const int grp = tid / kLanes, col = 4 * (tid % kLanes);
   const int rt = r / tile;
-  // The first piece may lie in its share's second slot, the others in the first.
-  auto row_of = [&](int i) {
-    const int64_t slot = i == 0 ? pieces.y : (pieces.y & ~1) + 2 * i;
-    return (slot * a.n_rt + rt) * tile + (r - rt * tile);
-  };
+  auto row_of = [&](int i) { return (int64_t(pieces.y + i) * a.n_rt + rt) * tile + (r - rt * tile); };
   float base = kNoBase, l = 0.f;
   f32x4_t o = f32x4_t{0.f, 0.f, 0.f, 0.f};
   constexpr int kAhead = 4;
@@ -697,7 +703,8 @@ hipError_t launch(const PagedArgs& a, hipStream_t s) {
       hipLaunchKernelGGL((attn_kernel<D, kF32, kFmt, 2, false, true, 4>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
   }
-  const dim3 grid(uint32_t(a.n_wg) * a.n_rt);
+  // At most n_wg pieces of a full share and one shorter one per head.
+  const dim3 grid(uint32_t((a.n_wg + units + 7) / 8 * 8) * a.n_rt);
   if (tile == 16 && a.stream_nt)
     hipLaunchKernelGGL((attn_kernel<D, kF32, kFmt, 1, true, false, 4>), grid, dim3(256), 0, s, a);
   else if (tile == 16)
