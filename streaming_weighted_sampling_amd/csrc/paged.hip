@@ -372,6 +372,8 @@ __global__ __launch_bounds__(256, kF32 ? 4 : 6) void append_kernel(PagedArgs a) 
         }
       }
     }
+    // In place the count may change only when every wavefront has read it.
+    __syncthreads();
     if (tid == 0 && !a.bump) a.lens_out[unit] = end;
   }
   if (bad) paged_status(a.status, kStatusNonFinite);
