@@ -353,13 +353,18 @@ nx_status nx_read_device_status(const nx_desc* desc);
  * matrix instruction that sums over rows.)
  *
  * Conventions are those above, and: bases and strides of q, k, v, out and the
- * cache arrays are multiples of 16 bytes (NX_EUNSUPPORTED otherwise).  A
- * sequence whose row range, row count or page number is out of range is skipped
- * (nx_paged_attn: its output rows are unspecified) and sets the bad-item bit of
- * the device status.  A call's pages are distinct for the (sequence, head)s that
- * it writes; pages that are only read may be shared.  The per-stage profiler
- * covers the eviction stages only.  With NX_DEBUG set these calls are
- * synchronous too.
+ * cache arrays are multiples of 16 bytes (NX_EUNSUPPORTED otherwise).  What only
+ * the device can see sets the bad-item bit of the device status: a sequence
+ * whose row range or row count is out of range is skipped (nx_paged_attn: its
+ * output rows are unspecified); of a block whose page number is out of range
+ * nx_paged_append stores nothing (the count still advances), nx_paged_gather
+ * writes nothing, and nx_paged_attn reads page 0 in its place.  A call's pages
+ * are distinct for the (sequence, head)s that it writes; pages that are only
+ * read may be shared.  Outputs that overlap another array of the call are
+ * refused (NX_EALIAS), also the small ones and the workspace.  Without rows a call
+ * does nothing.  Calls that may run at the same time have workspaces of their own.
+ * The per-stage profiler covers the eviction stages only.  With NX_DEBUG set these
+ * calls are synchronous too.
  */
 enum { NX_CACHE_E4M3 = 0, NX_CACHE_I8 = 1 };   /* 8-bit codes: OCP e4m3, signed integer */
 enum { NX_ROPE_HALF = 0, NX_ROPE_PAIRS = 1 };  /* pairs (i, i + rot/2), or (2i, 2i + 1) */
@@ -443,9 +448,10 @@ nx_status nx_qk_norm_rope(const nx_desc* desc, const nx_rope* rope, int32_t n_ro
  * A row is rotated in fp64 and rounded to the call's dtype; when its block is full
  * the block's scale is s = amax * (1 / M) (M = 448 or 127; a block whose largest
  * magnitude is at most 2^-100 has s = 0 and codes 0) and its codes are
- * x * ((1 / amax) * M) rounded to nearest even, each operation rounded to fp32.  A non-finite element is stored as 0 and
- * recorded in the device status (NX_ENONFINITE).  A sequence whose rows do not fit
- * its table is left as it was and marked bad.
+ * x * ((1 / amax) * M) rounded to nearest even, each operation rounded to fp32.  A
+ * non-finite element is stored as 0 and recorded in the device status
+ * (NX_ENONFINITE).  A sequence whose rows do not fit its table is left as it was and
+ * marked bad.
  */
 nx_status nx_paged_append(const nx_paged* cache, const nx_rope* rope, const nx_rows* k,
                           const nx_rows* v, int32_t n_rows, const int32_t* new_start,
@@ -456,7 +462,8 @@ nx_status nx_paged_append(const nx_paged* cache, const nx_rope* rope, const nx_r
  * sequence with m queries sees the rows t <= n - m + i of a head of n rows (the
  * queries' own rows are the last m; all are seen at m = 1).  A query that sees no
  * row gives a zero output and lse = -infinity.  Query head g reads KV head
- * g / (n_q_heads / n_kv_heads).
+ * g / (n_q_heads / n_kv_heads).  |scale q . k| must stay below 10^29; a row of q with
+ * a non-finite element has an unspecified output, the other rows have theirs.
  *   q, out     n_rows rows of n_q_heads heads (they must not overlap)
  *   q_start    nullable [n_seqs + 1] int32 (device): sequence s has the rows q_start[s] ..
  *              q_start[s + 1] - 1, at most max_q; NULL: max_q rows each.  Rows of no sequence

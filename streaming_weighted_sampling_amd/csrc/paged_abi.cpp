@@ -11,6 +11,7 @@ using namespace nx;
 namespace {
 
 constexpr int64_t kMaxCacheRows = int64_t(1) << 24;
+constexpr int64_t kMaxGrid = int64_t(1) << 23;   // workgroups of up to 512 threads: 2^32 threads
 constexpr int64_t kCUs = 256;
 // Workgroups per CU that an attention call is cut into.  16-row tiles: one
 // where that leaves four pieces a head (it reads at the memory's rate already,
@@ -85,6 +86,12 @@ nx_status check_rope(const nx_rope* r, int32_t head_dim) {
   return NX_OK;
 }
 
+// Whether an output meets the rotation's arrays.
+bool meets(const Range& out, const nx_rope* r, int64_t n_rows) {
+  return r != nullptr && (overlap(out, bytes_at(r->cos_sin, int64_t(r->n_pos) * r->rot_dim * 4)) ||
+                          overlap(out, bytes_at(r->positions, r->positions != nullptr ? n_rows * 4 : 0)));
+}
+
 nx_status check_shape(const nx_paged* c) {
   if (c == nullptr) return NX_EINVAL;
   if (c->n_seqs < 1 || c->n_kv_heads < 1 || c->n_q_heads < c->n_kv_heads || c->n_q_heads % c->n_kv_heads)
@@ -154,6 +161,7 @@ nx_status make_cut(const nx_paged* c, int64_t max_tokens, int64_t max_q, Cut* ou
   const int64_t per_cu = tile == 16 && units * kPiecesPerHead <= kCUs ? 1 : 2;
   const int64_t most = std::max<int64_t>(8, kCUs * per_cu / n_rt);
   const int64_t n_wg = std::min(most, (blocks + kMinShare - 1) / kMinShare);
+  if ((n_wg + units + 16) * n_rt >= kMaxGrid) return NX_EUNSUPPORTED;
   *out = {tile, n_rt, (n_wg + 7) / 8 * 8, blocks * kBlock * 2 * c->head_dim,
           max_tokens <= (units >= kManyHeads ? 2 * kWholeTokens : kWholeTokens)};
   return NX_OK;
@@ -196,9 +204,19 @@ nx_status nx_qk_norm_rope(const nx_desc* desc, const nx_rope* rope, int32_t n_ro
     if (!same_rows(k, out_k) && overlap(sk, sok)) return NX_EALIAS;
     if (overlap(soq, sk) || overlap(soq, sok) || overlap(sok, sq)) return NX_EALIAS;
   }
+  for (const RowSet* o : {&soq, &sok}) {
+    if (o == &sok && k == nullptr) break;
+    const Range r = o->range();
+    if (meets(r, rope, n_rows) || overlap(r, bytes_at(q_weight, q_weight != nullptr ? d * esz : 0)) ||
+        overlap(r, bytes_at(k_weight, k_weight != nullptr ? d * esz : 0)) ||
+        overlap(r, bytes_at(desc->workspace, 256)))
+      return NX_EALIAS;
+  }
   if (!aligned(q_weight) || !aligned(k_weight)) return NX_EUNSUPPORTED;
   if (desc->workspace == nullptr || desc->workspace_bytes < 256) return NX_EWORKSPACE;
   if (n_rows == 0) return NX_OK;
+  if (int64_t(n_rows) * (int64_t(desc->n_q_heads) + desc->n_kv_heads) / (4096 / d) >= kMaxGrid - 1)
+    return NX_EUNSUPPORTED;
   NormArgs a;
   std::memset(&a, 0, sizeof(a));
   if (rope != nullptr) a.rope = *rope;
@@ -228,8 +246,7 @@ nx_status nx_paged_append(const nx_paged* cache, const nx_rope* rope, const nx_r
   nx_status st = check_cache(cache);
   if (st != NX_OK) return st;
   if (n_rows < 0 || max_new < 0 || max_new > kMaxCacheRows) return NX_EINVAL;
-  // The launch's workgroups are numbered in 31 bits.
-  if ((int64_t(max_new) / kBlock + 8) * cache->n_kv_heads > INT32_MAX) return NX_EUNSUPPORTED;
+  if ((int64_t(max_new) / kBlock + 8) * cache->n_kv_heads >= kMaxGrid) return NX_EUNSUPPORTED;
   if (new_start == nullptr && int64_t(cache->n_seqs) * max_new > n_rows) return NX_EINVAL;
   if ((st = check_rope(rope, cache->head_dim)) != NX_OK) return st;
   const int64_t esz = elem_size(cache->dtype), d = cache->head_dim;
@@ -241,17 +258,21 @@ nx_status nx_paged_append(const nx_paged* cache, const nx_rope* rope, const nx_r
   const int64_t units = int64_t(cache->n_seqs) * cache->n_kv_heads;
   const Range lens = bytes_at(cache->lens, units * 4);
   const Range lout = bytes_at(lens_out != nullptr ? lens_out : cache->lens, units * 4);
-  const Range ins[] = {sk.range(), sv.range(), bytes_at(cache->table, units * cache->max_pages * 4)};
+  // lens_out is written while some workgroups still read the counts and starts.
+  const Range ins[] = {sk.range(), sv.range(), bytes_at(cache->table, units * cache->max_pages * 4),
+                       bytes_at(head_new, head_new != nullptr ? units * 4 : 0),
+                       bytes_at(new_start, new_start != nullptr ? (int64_t(cache->n_seqs) + 1) * 4 : 0),
+                       bytes_at(cache->workspace, 256)};
   for (int i = 0; i < 6; ++i) {
     for (int j = i + 1; j < 6; ++j)
       if (overlap(cr.r[i], cr.r[j])) return NX_EALIAS;
     for (const Range& x : ins)
       if (overlap(cr.r[i], x)) return NX_EALIAS;
-    if (overlap(cr.r[i], lens) || overlap(cr.r[i], lout)) return NX_EALIAS;
+    if (overlap(cr.r[i], lens) || overlap(cr.r[i], lout) || meets(cr.r[i], rope, n_rows)) return NX_EALIAS;
   }
   for (const Range& x : ins)
     if (overlap(lout, x)) return NX_EALIAS;
-  if (lout.lo != lens.lo && overlap(lout, lens)) return NX_EALIAS;
+  if (meets(lout, rope, n_rows) || (lout.lo != lens.lo && overlap(lout, lens))) return NX_EALIAS;
   PagedArgs a = base_args(cache);
   if (rope != nullptr) a.rope = *rope;
   a.k = *k;
@@ -272,7 +293,7 @@ nx_status nx_paged_attn(const nx_paged* cache, const nx_rows* q, const nx_rows* 
   nx_status st = check_cache(cache);
   if (st != NX_OK) return st;
   if (n_rows < 0 || !std::isfinite(scale) || scale < 0.f) return NX_EINVAL;
-  if (q_start == nullptr && int64_t(cache->n_seqs) * max_q > n_rows) return NX_EINVAL;
+  if (q_start == nullptr && n_rows > 0 && int64_t(cache->n_seqs) * max_q > n_rows) return NX_EINVAL;
   Cut cut;
   if ((st = make_cut(cache, max_tokens, max_q, &cut)) != NX_OK) return st;
   const int64_t esz = elem_size(cache->dtype), d = cache->head_dim;
@@ -281,10 +302,18 @@ nx_status nx_paged_attn(const nx_paged* cache, const nx_rows* q, const nx_rows* 
   if (overlap(sq, so)) return NX_EALIAS;
   const CacheRanges cr = cache_ranges(cache);
   const Range lse = bytes_at(out_lse, out_lse != nullptr ? int64_t(n_rows) * cache->n_q_heads * 4 : 0);
+  const int64_t units = int64_t(cache->n_seqs) * cache->n_kv_heads;
+  const Range ro = so.range(), ins[] = {
+      bytes_at(cache->table, units * cache->max_pages * 4), bytes_at(cache->lens, units * 4),
+      bytes_at(q_start, q_start != nullptr ? (int64_t(cache->n_seqs) + 1) * 4 : 0),
+      bytes_at(cache->workspace, int64_t(cut_bytes(cache, cut)))};
   for (const Range& x : cr.r)
-    if (overlap(so.range(), x) || overlap(lse, x)) return NX_EALIAS;
-  if (overlap(lse, sq.range()) || overlap(lse, so.range())) return NX_EALIAS;
+    if (overlap(ro, x) || overlap(lse, x)) return NX_EALIAS;
+  for (const Range& x : ins)
+    if (overlap(ro, x) || overlap(lse, x)) return NX_EALIAS;
+  if (overlap(lse, sq.range()) || overlap(lse, ro)) return NX_EALIAS;
   if (cache->workspace_bytes < cut_bytes(cache, cut)) return NX_EWORKSPACE;
+  if (n_rows == 0) return NX_OK;
   PagedArgs a = base_args(cache);
   a.q = *q;
   a.out = *out;
@@ -325,6 +354,10 @@ nx_status nx_paged_gather(const nx_paged* cache, int32_t max_tokens, void* out_k
   const CacheRanges cr = cache_ranges(cache);
   if (overlap(ok, ov)) return NX_EALIAS;
   for (const Range& x : cr.r)
+    if (overlap(ok, x) || overlap(ov, x)) return NX_EALIAS;
+  const int64_t units = int64_t(cache->n_seqs) * hk;
+  for (const Range& x : {bytes_at(cache->table, units * cache->max_pages * 4), bytes_at(cache->lens, units * 4),
+                         bytes_at(cache->workspace, 256)})
     if (overlap(ok, x) || overlap(ov, x)) return NX_EALIAS;
   if (max_tokens == 0) return NX_OK;
   PagedArgs a = base_args(cache);

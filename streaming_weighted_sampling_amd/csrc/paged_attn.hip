@@ -24,7 +24,8 @@
 //
 // Roundings.  q enters as f16 after a power-of-two scaling of its row (largest
 // magnitude in [2^13, 2^14)): bf16 elements are exact down to 2^-20 of the
-// row's largest and off by at most 2^-38 of it below, fp32 rows use a second f16 term for the remainder (22 bits).
+// row's largest and off by at most 2^-38 of it below, fp32 rows use a second f16
+// term for the remainder (22 bits).
 // p enters as f16 (relative 2^-11, against the bf16 result's 2^-8), or as two
 // f16 terms for fp32 rows.  Sums, references and accumulators are fp32.
 #include "paged.hpp"
@@ -257,7 +258,8 @@ __device__ inline void exponentiate(State<D, RT>& st, float back, float (&z)[RT]
   }
 }
 
-// The query rows of one tile: where row (rt, c) lies, or null past the last.
+// Bytes from the array's start to query row r of a sequence's KV head h (row r is query
+// r / group, head r % group of the group).
 template <bool kF32>
 __device__ inline int64_t row_offset(const PagedArgs& a, const nx_rows& rows, const Job& job, int h, int r) {
   const int i = r / a.group, gh = r - i * a.group;

@@ -68,6 +68,8 @@ class DecodeCache:
         """Replaces the rows: k, v [n_seqs, n_kv_heads, rows, D], keys already rotated (a prompt's
         rows, or the out_k / out_v of a first event)."""
         n, hk, rows, d = k.shape
+        if n != self.n_seqs or v.shape != k.shape:
+            raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)}: rows of {self.n_seqs} sequences expected")
         if rows > self.capacity:
             raise ValueError(f"{rows} rows, capacity {self.capacity}")
         self.cache.lens.zero_()
@@ -78,10 +80,12 @@ class DecodeCache:
 
     def step(self, q, k, v, positions=None):
         """One new token per sequence: q [n_seqs, n_q_heads, D], k, v [n_seqs, n_kv_heads, D] as
-        projected, positions int32 [n_seqs].  Returns out [n_seqs, n_q_heads, D], which the next
+        projected, positions int32 [n_seqs] (with rope).  Returns out [n_seqs, n_q_heads, D], which the next
         step overwrites."""
         if self.rows + 1 > self.capacity:
             raise ValueError("the cache is full: evict first")
+        if (self.rope is None) != (positions is None):
+            raise ValueError("positions go with rope")
         cfg = self.cfg
         q_rot = self.ring[:, :, self.queries % cfg.window]
         normed = self.k_weight is not None

@@ -222,8 +222,8 @@ def nx_qk_norm_rope(cfg, q, k=None, *, workspace, q_weight=None, k_weight=None, 
     if rope is None and positions is not None:
         raise ValueError("positions without rope")
     r = None if rope is None else rope._struct(positions, n, dev)
-    if workspace.get_device() != dev:
-        raise ValueError(f"the workspace must be on {q.device}")
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous on {q.device}")
     c = NxDesc()
     c.n_q_heads, c.n_kv_heads, c.head_dim, c.dtype = hq, hk, d, _DTYPES.get(cfg.dtype, 99)
     c.workspace, c.workspace_bytes, c.stream = workspace.data_ptr(), workspace.nbytes, _stream(stream, dev)
@@ -275,7 +275,7 @@ def nx_paged_attn(cfg, cache, q, *, workspace, max_tokens, max_q=None, q_start=N
     if out is None:
         out = torch.empty(n, hq, cfg.head_dim, dtype=cfg.dtype, device=q.device)
     ro = _rows(cfg, out, "out", hq, dev, n)
-    max_q = _per_seq(cache, n, max_q, q_start, "max_q", "q_start")
+    max_q = _per_seq(cache, n, max_q, q_start, "max_q", "q_start") if n else 1      # no rows: nothing is done
     if scale is not None and not scale > 0:
         raise ValueError("scale must be positive")
     qs = _opt(q_start, "q_start", (cache.n_seqs + 1,), torch.int32, dev)

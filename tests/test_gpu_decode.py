@@ -114,3 +114,11 @@ def test_decode_cache_refuses_what_it_cannot_hold():
     out = dec.step(q, k, k)              # the first row of an empty cache: attention is that row
     dec.check()
     assert torch.equal(out, k.repeat_interleave(2, 1))
+    with pytest.raises(ValueError, match="sequences"):
+        dec.load(*[torch.zeros(2, 2, 8, 64, dtype=torch.bfloat16, device=DEV)] * 2)
+    with pytest.raises(ValueError, match="positions"):
+        dec.step(q, k, k, torch.zeros(1, dtype=torch.int32, device=DEV))
+    turned = nx.DecodeCache(cfg, 1, 64, 32, 1, page_blocks=1, rope=nx.Rope(nx.rope_table(9, 64, device=DEV)),
+                            device=DEV)
+    with pytest.raises(ValueError, match="positions"):
+        turned.step(q, k, k)

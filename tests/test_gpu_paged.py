@@ -595,3 +595,102 @@ def test_two_streams_with_their_own_workspaces():
                                             stream=streams[i]))
     torch.cuda.synchronize()
     assert all(torch.equal(o, ref) for side in outs for o in side)
+
+
+def test_calls_without_rows_do_nothing():
+    cache = Cache(2, 1, 2, 64, "bf16", "e4m3", 1, 2)
+    cache.fill([40, 3])
+    none = torch.zeros(0, 1, 64, dtype=torch.bfloat16, device=DEV)
+    before = cache.c.lens.clone()
+    nx.nx_paged_append(cache.cfg, cache.c, none, none, workspace=cache.ws)
+    assert nx.nx_paged_attn(cache.cfg, cache.c, none.expand(0, 2, 64), workspace=cache.ws, max_tokens=40).numel() == 0
+    nx.nx_qk_norm_rope(cache.cfg, none.expand(0, 2, 64), none, workspace=cache.ws)
+    start = torch.zeros(3, dtype=torch.int32, device=DEV)
+    q = torch.full((3, 2, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    out = torch.full_like(q, 3.0)
+    nx.nx_paged_attn(cache.cfg, cache.c, q, workspace=cache.ws, max_tokens=40, max_q=1, q_start=start, out=out)
+    cache.check()
+    assert torch.equal(cache.c.lens, before) and (out == 3.0).all()
+
+
+def test_many_heads_of_uneven_lengths():
+    """More heads than workgroups wanted, and more than stay in registers, some empty; the bound on the
+    lengths forces pieces."""
+    cache = Cache(150, 2, 1, 64, "bf16", "int8", 1, 6, max_q=1)
+    lens = [(37 * i) % 190 if i % 7 else 0 for i in range(300)]
+    cache.fill(lens, garbage=False)
+    q = _randn(61, 150, 2, 64, dtype="bf16")
+    for most in (190, 6000):
+        ws = nx.new_paged_workspace(cache.cfg, cache.c, most)
+        out = nx.nx_paged_attn(cache.cfg, cache.c, q, workspace=ws, max_tokens=most)
+        nx.nx_read_device_status(cache.cfg, ws)
+        _check_attn(cache, q, [1] * 150, out)
+
+
+def test_one_workspace_serves_calls_of_different_shapes():
+    """A workspace made for the largest call, used by others in between: partials and the notes on
+    the cut belong to one call."""
+    big = Cache(1, 2, 8, 128, "bf16", "e4m3", 4, 20, max_q=16)
+    big.fill([2500, 2431])
+    small = Cache(3, 2, 1, 64, "bf16", "int8", 1, 50)
+    small.fill([1500, 0, 33, 1111, 1499, 64])
+    qb, qs = _randn(71, 16, 16, 128, dtype="bf16"), _randn(72, 3, 2, 64, dtype="bf16")
+    for _ in range(3):
+        for cache, q, most, counts in ((big, qb, 2500, [16]), (small, qs, 1500, [1, 1, 1]), (big, qb[:1], 2500, [1])):
+            out = nx.nx_paged_attn(cache.cfg, cache.c, q, workspace=big.ws, max_tokens=most)
+            _check_attn(cache, q, counts, out)
+    nx.nx_read_device_status(big.cfg, big.ws)
+
+
+def test_two_graphs_share_a_workspace():
+    """Captured attention calls of different cuts, replayed in turn with eager calls between."""
+    long = Cache(1, 2, 4, 128, "bf16", "int8", 4, 20)
+    long.fill([2500, 1601])
+    many = Cache(9, 2, 2, 64, "bf16", "e4m3", 2, 25)
+    many.fill([(97 * i) % 1500 for i in range(18)])
+    q = [_randn(81, 1, 8, 128, dtype="bf16"), _randn(82, 9, 4, 64, dtype="bf16")]
+    outs, graphs = [torch.empty_like(x) for x in q], []
+
+    def call(i):
+        cache = (long, many)[i]
+        nx.nx_paged_attn(cache.cfg, cache.c, q[i], workspace=long.ws, max_tokens=(2500, 1500)[i], out=outs[i])
+
+    need = nx.paged_workspace_bytes(many.cfg, many.c, 1500)
+    if long.ws.nbytes < need:
+        long.ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    for i in range(2):
+        call(i)
+    torch.cuda.synchronize()
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            call(i)
+    for turn in range(3):
+        for i in (0, 1, 1, 0):
+            outs[i].fill_(9.0)
+            graphs[i].replay()
+            _check_attn((long, many)[i], q[i], [1] * len(q[i]), outs[i])
+        call(turn % 2)
+        torch.cuda.synchronize()
+    long.check()
+
+
+def test_debug_mode_raises_at_the_call(monkeypatch):
+    monkeypatch.setenv("NX_DEBUG", "1")
+    cache = Cache(1, 1, 2, 64, "bf16", "int8", 1, 2)
+    rows = _randn(91, 3, 1, 64, dtype="bf16")
+    nx.nx_paged_append(cache.cfg, cache.c, rows, rows, workspace=cache.ws)
+    assert nx.nx_paged_attn(cache.cfg, cache.c, rows[:1].expand(1, 2, 64), workspace=cache.ws,
+                            max_tokens=3).isfinite().all()
+    nx.nx_paged_gather(cache.cfg, cache.c, workspace=cache.ws, max_tokens=3)
+    nx.nx_qk_norm_rope(cache.cfg, rows.repeat(1, 2, 1), workspace=cache.ws)
+    rows[1, 0, 5] = float("inf")
+    with pytest.raises(nx.NexusError, match="NONFINITE"):
+        nx.nx_paged_append(cache.cfg, cache.c, rows, rows, workspace=cache.ws)
+    with pytest.raises(nx.NexusError, match="NONFINITE"):
+        cache.check()                    # still recorded; reading it clears it
+    cache.c.lens.fill_(65)
+    with pytest.raises(nx.NexusError, match="EINVAL"):
+        nx.nx_paged_attn(cache.cfg, cache.c, rows[:1].expand(1, 2, 64), workspace=cache.ws, max_tokens=64)
+    with pytest.raises(nx.NexusError, match="EINVAL"):
+        nx.nx_paged_gather(cache.cfg, cache.c, workspace=cache.ws, max_tokens=64)

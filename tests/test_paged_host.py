@@ -99,6 +99,12 @@ def test_append_arguments(lib):
     assert call(c=_ws(k_scale=FAKE + 4096)) == EALIAS
     assert call(out=FAKE + 7 * GB + 4) == EALIAS          # shifted against lens
     assert call(out=FAKE + 6 * GB) == EALIAS              # the table
+    assert call(head_new=FAKE + 7 * GB) == EALIAS         # lens, advanced in place, as the counts to add
+    assert call(start=FAKE + 41 * GB, out=FAKE + 41 * GB + 16) == EALIAS
+    assert call(out=FAKE + 8 * GB) == EALIAS              # the status word
+    assert call(k=_r(20, row=1 << 25)) == EUNSUP          # a row stride of 64 MB
+    inside = NxRope(FAKE + 4096, None, 10, 64, 0)         # a table inside the codes
+    assert call(rope=inside) == EALIAS
     for kw, code in ((dict(rot_dim=24), EUNSUP), (dict(rot_dim=144), EINVAL), (dict(rot_dim=-16), EINVAL),
                      (dict(n_pos=0), EINVAL), (dict(style=2), EINVAL), (dict(cos_sin=None), EINVAL),
                      (dict(cos_sin=FAKE + 4), EUNSUP)):
@@ -121,7 +127,13 @@ def test_attention_arguments(lib):
     assert call(o=_r(21, 4096, 0)) == EINVAL
     assert call(o=_r(4, 4096)) == EALIAS                  # into the tail
     assert call(lse=FAKE + 21 * GB) == EALIAS
+    for lo in (6, 7, 8):                                  # table, lens, workspace
+        assert call(lse=FAKE + lo * GB) == EALIAS
+        assert call(o=_r(lo, 4096)) == EALIAS
+    assert call(start=FAKE + 21 * GB + 8192) == EALIAS
     assert call() == EWORK                                # 256 bytes hold no partials
+    assert call(n=0, m=0) == EINVAL
+    assert call(n=1 << 30, m=1 << 20, start=FAKE + 40 * GB) == EUNSUP      # rows of one head: 2^22
     # slices of one projection do not overlap: the call gets as far as the workspace
     one = NxRows(FAKE + 20 * GB, 3 * 4096, 128)
     two = NxRows(FAKE + 20 * GB + 2 * 4096, 3 * 4096, 128)
@@ -139,6 +151,7 @@ def test_gather_arguments(lib):
     assert call(v=FAKE + 30 * GB + 4096) == EALIAS
     assert call(k=FAKE) == EALIAS
     assert call(k=FAKE + 30 * GB + 8) == EUNSUP
+    assert call(v=FAKE + 7 * GB) == EALIAS                # the row counts
     assert call(t=0, hs=0, ss=0) == _lib.NX_OK            # nothing to do
 
 
@@ -166,6 +179,7 @@ def test_norm_rope_arguments(lib):
     assert call(wk=FAKE) == EINVAL                        # a weight without k
     assert call(wq=FAKE + 4) == EUNSUP
     assert call(oq=NxRows(FAKE + 20 * GB + 256, 4096, 128)) == EALIAS
+    assert call(oq=_r(0, 4096)) == EALIAS                 # the workspace
     assert call(oq=_r(21, 128)) == EINVAL
     assert call(k=_r(22), ok=_r(21)) == EALIAS            # out_k on out_q
 
