@@ -15,17 +15,21 @@ constexpr int64_t kMaxGrid = int64_t(1) << 23;   // workgroups of up to 512 thre
 constexpr int64_t kCUs = 256;
 // Workgroups per CU that an attention call is cut into.  16-row tiles: one
 // where that leaves four pieces a head (it reads at the memory's rate already,
-// with fewer pieces to merge: 8 heads of 32768 rows 19.8 us, two 21.5), else
-// two (128 uneven heads: 66 us, one 75).  32-row tiles: two (registers).
+// with fewer pieces to merge: 8 heads of 32768 rows 19.8 us, two 21.4), else
+// two (128 uneven heads: 66 us, one 74).  32-row tiles: two (registers).
 constexpr int64_t kPiecesPerHead = 4;
-constexpr int64_t kMinShare = 4;        // blocks of a full piece: one per wavefront
-// Heads of up to this many rows are taken whole by a workgroup each (8 heads of
-// 1024 rows: 9.5 us, in shares 9.3; of 819: 9.2 and 12.3), of up to twice as many
-// where there are kManyHeads of them (128 of 2048: 15.8 and 19.3).
-constexpr int64_t kWholeTokens = 1024, kManyHeads = 64;
+// Fewest blocks of a full piece: one per wavefront (8 heads of 6810 rows: 12.4 us,
+// with eight blocks 13.6).
+constexpr int64_t kMinShare = 4;
+// Heads of up to kWholeTokens rows are taken whole by a workgroup each (8 heads of
+// 819 rows: 8.9 us, in shares 9.2; of 1536: 11.5 and 9.6), of up to kWholeMany
+// rows where they nearly fill one round of workgroups (128 heads of 2560 rows:
+// 18.5 and 23.0, of 3200: 28.7 and 26.2; 256 of 2560: 34.7 and 36.6; but 64 of
+// 2048: 15.0 and 14.2, 384 of 2048: 46.0 and 42.6).
+constexpr int64_t kWholeTokens = 1024, kWholeMany = 2560, kManyHeads = 96;
 // Codes of more than this many bytes are read past the caches (a quarter of
 // the 256 MB cache: other layers' calls lie between two reads of the same
-// bytes; 268 MB: 50.8 us, cached 57.2, 134 MB: 30.3 and 33.7).
+// bytes; 268 MB: 51.1 us, cached 56.9, 134 MB: 30.5 and 34.7, 67 MB: 21.0 and 19.9).
 constexpr int64_t kStreamBytes = int64_t(64) << 20;
 
 int32_t elem_size(int32_t dtype) { return dtype == NX_BF16 ? 2 : 4; }
@@ -163,7 +167,7 @@ nx_status make_cut(const nx_paged* c, int64_t max_tokens, int64_t max_q, Cut* ou
   const int64_t n_wg = std::min(most, (blocks + kMinShare - 1) / kMinShare);
   if ((n_wg + units + 16) * n_rt >= kMaxGrid) return NX_EUNSUPPORTED;
   *out = {tile, n_rt, (n_wg + 7) / 8 * 8, blocks * kBlock * 2 * c->head_dim,
-          max_tokens <= (units >= kManyHeads ? 2 * kWholeTokens : kWholeTokens)};
+          max_tokens <= (units >= kManyHeads && units <= kCUs ? kWholeMany : kWholeTokens)};
   return NX_OK;
 }
 // Workspace: status word, the heads' pieces, partials.
