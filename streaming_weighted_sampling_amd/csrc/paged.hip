@@ -1,9 +1,13 @@
 // The decode step around the attention: norm and rotation of query and key
 // heads, appending rows to the paged 8-bit cache, and reading it back.
+#include <type_traits>
+
 #include "paged.hpp"
 
 namespace nx {
 namespace {
+
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 // The 16 elements of one row that one thread holds, as two runs of 8, chosen
 // so that a rotation pair never crosses threads: threads j < rot / 16 hold
@@ -191,10 +195,10 @@ __device__ inline uint32_t codes4(float a, float b, float c, float d) {
 // The product is rounded by itself, as the definition has it: fused with the
 // rounding addition it would move ties.
 template <int kFmt>
-__device__ inline uint2 codes8(const float (&x)[8], float inv) {
+__device__ inline u32x2_t codes8(const float (&x)[8], float inv) {
 #pragma clang fp contract(off)
-  return make_uint2(codes4<kFmt>(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
-                    codes4<kFmt>(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
+  return {codes4<kFmt>(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+          codes4<kFmt>(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv)};
 }
 
 // Scale and inverse of a block whose largest magnitude is `top`.
@@ -212,7 +216,7 @@ __device__ inline void block_scale(float top, float& scale, float& inv) {
 // one thread).  V: 8 rows x 2 elements per thread, which is 16 consecutive
 // bytes of the stored block.  Memory bound on long prompts: a block's codes
 // wait for its largest magnitude, so its 32 rows stay in registers and are read
-// once (four prompts of 8192 to 16384 tokens, 8 bf16 heads of 128, 344 MB: 81 us, 4.2 TB/s;
+// once (four prompts of 8192 to 16384 tokens, 8 bf16 heads of 128, 344 MB: 79 us, 4.3 TB/s;
 // a copy of as many bytes 69).  One token for 16 sequences: 5.6 us, launch and
 // the chain lengths -> tail -> maximum -> codes.
 template <int D, bool kF32, int kFmt>
@@ -343,10 +347,17 @@ __global__ __launch_bounds__(256, kF32 ? 4 : 6) void append_kernel(PagedArgs a) 
       const int64_t slot = (int64_t(page) << a.page_shift) + (b & ((1 << a.page_shift) - 1));
       char* kc = static_cast<char*>(a.c.k_codes) + slot * kBlock * D;
       char* vc = static_cast<char*>(a.c.v_codes) + slot * kBlock * D;
-      *reinterpret_cast<uint2*>(kc + krow * D + r.d0) = codes8<kFmt>(kx, kinv);
-      *reinterpret_cast<uint2*>(kc + krow * D + r.d1) = codes8<kFmt>(ky, kinv);
-      const uint2 v0 = codes8<kFmt>(vx, vinv), v1 = codes8<kFmt>(vy, vinv);
-      *reinterpret_cast<uint4*>(vc + (vg * D + vd) * 8) = make_uint4(v0.x, v0.y, v1.x, v1.y);
+      const u32x2_t k0 = codes8<kFmt>(kx, kinv), k1 = codes8<kFmt>(ky, kinv);
+      const u32x2_t v0 = codes8<kFmt>(vx, vinv), v1 = codes8<kFmt>(vy, vinv);
+      const u32x4_t v = {v0.x, v0.y, v1.x, v1.y};
+      const Buf kb(kc, kBlock * D), vb(vc, kBlock * D);
+      auto put = [&](auto aux) {
+        __builtin_amdgcn_raw_buffer_store_b64(k0, kb.r, krow * D + r.d0, 0, aux.value);
+        __builtin_amdgcn_raw_buffer_store_b64(k1, kb.r, krow * D + r.d1, 0, aux.value);
+        __builtin_amdgcn_raw_buffer_store_b128(v, vb.r, (vg * D + vd) * 8, 0, aux.value);
+      };
+      if (a.stream_nt) put(std::integral_constant<int, kNonTemporal>{});
+      else put(std::integral_constant<int, 0>{});
       if (tid == 0) {
         a.c.k_scale[slot] = kscale;
         a.c.v_scale[slot] = vscale;

@@ -23,12 +23,12 @@ struct PagedArgs {
   int32_t bump;            // append: 1: a second launch advances lens_out == lens
   int32_t append_by8;      // append: 1: a range's heads are eight workgroups apart
   int32_t page_shift;      // log2(page_blocks)
+  int32_t stream_nt;       // 1: the codes are read or written past the caches
   uint32_t* status;
   // attention
   int32_t group, max_q, n_rt, n_wg;   // query-row tiles, workgroups wanted
   int32_t min_share;       // fewest blocks of a full piece
   int32_t whole;           // 1: a workgroup per head, no pieces
-  int32_t stream_nt;       // 1: the codes are read past the caches
   float scale_log2;        // scale * log2(e)
   float* lse;
   int2* pieces;            // [units]: a head's pieces (0: written at once) and its first partial

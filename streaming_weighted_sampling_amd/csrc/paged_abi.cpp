@@ -27,9 +27,10 @@ constexpr int64_t kMinShare = 4;
 // 18.5 and 23.0, of 3200: 28.7 and 26.2; 256 of 2560: 34.7 and 36.6; but 64 of
 // 2048: 15.0 and 14.2, 384 of 2048: 46.0 and 42.6).
 constexpr int64_t kWholeTokens = 1024, kWholeMany = 2560, kManyHeads = 96;
-// Codes of more than this many bytes are read past the caches (a quarter of
-// the 256 MB cache: other layers' calls lie between two reads of the same
-// bytes; 268 MB: 51.1 us, cached 56.9, 134 MB: 30.5 and 34.7, 67 MB: 21.0 and 19.9).
+// Codes of more than this many bytes are read and written past the caches (a
+// quarter of the 256 MB cache: other layers' calls lie between two uses of the
+// same bytes).  Attention over 268 MB: 51.1 us, cached 56.9, 134 MB: 30.5 and
+// 34.7, 67 MB: 21.0 and 19.9.  An append that writes 106 MB: 79 us, cached 81.
 constexpr int64_t kStreamBytes = int64_t(64) << 20;
 
 int32_t elem_size(int32_t dtype) { return dtype == NX_BF16 ? 2 : 4; }
@@ -286,6 +287,7 @@ nx_status nx_paged_append(const nx_paged* cache, const nx_rope* rope, const nx_r
   a.start = new_start;
   a.head_new = head_new;
   a.lens_out = lens_out != nullptr ? lens_out : cache->lens;
+  a.stream_nt = int64_t(n_rows) * cache->n_kv_heads * 2 * d > kStreamBytes;
   hipStream_t s = static_cast<hipStream_t>(cache->stream);
   if (launch_paged_append(a, s) != hipSuccess) return NX_EHIP;
   return debug_status(a.status, s, "paged_append");

@@ -694,3 +694,23 @@ def test_debug_mode_raises_at_the_call(monkeypatch):
         nx.nx_paged_attn(cache.cfg, cache.c, rows[:1].expand(1, 2, 64), workspace=cache.ws, max_tokens=64)
     with pytest.raises(nx.NexusError, match="EINVAL"):
         nx.nx_paged_gather(cache.cfg, cache.c, workspace=cache.ws, max_tokens=64)
+
+
+def test_a_long_prompt_equals_its_parts():
+    """One append of 67 MB of codes (written past the caches) against three smaller ones."""
+    n, hk, d = 66001, 8, 64
+    rows = _randn(95, 2, n, hk, d, dtype="bf16")
+    got = []
+    for cuts in ((0, n), (0, 20000, 40007, n)):
+        cache = Cache(1, hk, 1, d, "bf16", "int8", 8, -(-n // 256))
+        for lo, hi in zip(cuts, cuts[1:]):
+            nx.nx_paged_append(cache.cfg, cache.c, rows[0, lo:hi], rows[1, lo:hi], workspace=cache.ws)
+        cache.check()
+        got.append(nx.nx_paged_gather(cache.cfg, cache.c, workspace=cache.ws, max_tokens=n))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    for x, y in zip(rows, got[0]):       # off by at most half a code and the result's rounding
+        x = x.permute(1, 0, 2).float()
+        amax = torch.nn.functional.pad(x, (0, 0, 0, -n % 32)).view(hk, -1, 32 * d).abs().amax(-1)
+        bound = (amax / 254 * (1 + 2.0 ** -20)).repeat_interleave(32, 1)[:, :n, None] + x.abs() * 2.0 ** -7
+        assert ((y[0].float() - x).abs() <= bound).all()
