@@ -72,7 +72,7 @@ __device__ inline void rotate_runs(float (&x)[8], float (&y)[8], const float* cs
 // square sum is reduced over them.  Memory bound: every element is read and
 // written once, in 16-byte accesses (8192 rows of 64 + 8 bf16 heads of 128,
 // 304 MB: 59.6 us, 5.1 TB/s, the rate of a large copy).  16 rows of 32 + 8 heads
-// take 3.4 us, two launch latencies' worth.
+// take 3.4 us, most of it launch and one read's latency.
 template <int D, bool kF32>
 __global__ __launch_bounds__(256) void norm_rope_kernel(NormArgs a) {
   using E = Elem<kF32>;
