@@ -25,8 +25,14 @@ constexpr int64_t kMinShare = 4;
 // 819 rows: 8.9 us, in shares 9.2; of 1536: 11.5 and 9.6), of up to kWholeMany
 // rows where they nearly fill one round of workgroups (128 heads of 2560 rows:
 // 18.5 and 23.0, of 3200: 28.7 and 26.2; 256 of 2560: 34.7 and 36.6; but 64 of
-// 2048: 15.0 and 14.2, 384 of 2048: 46.0 and 42.6).
+// 2048: 15.0 and 14.2, 384 of 2048: 46.0 and 42.6).  From kRounds heads on the
+// rounds of workgroups even out by themselves, and every workgroup's search
+// through the heads for its piece costs more: whole up to kWholeRounds rows (1024
+// heads of 256 to 4096 rows: 115 and 133, of 512 to 16384: 411 and 469, 4096 of
+// 1024: 202 and 355; 512 of 512 to 16384: 231 and 210), with 32-row tiles up to a
+// quarter (32 query rows, 512 to 4096 rows: 141 and 172; 128, 512 to 8192: 686 and 569).
 constexpr int64_t kWholeTokens = 1024, kWholeMany = 2560, kManyHeads = 96;
+constexpr int64_t kWholeRounds = 16384, kRounds = 1024;
 // Codes of more than this many bytes are read and written past the caches (a
 // quarter of the 256 MB cache: other layers' calls lie between two uses of the
 // same bytes).  Attention over 268 MB: 51.1 us, cached 56.9, 134 MB: 30.5 and
@@ -167,8 +173,9 @@ nx_status make_cut(const nx_paged* c, int64_t max_tokens, int64_t max_q, Cut* ou
   const int64_t most = std::max<int64_t>(8, kCUs * per_cu / n_rt);
   const int64_t n_wg = std::min(most, (blocks + kMinShare - 1) / kMinShare);
   if ((n_wg + units + 16) * n_rt >= kMaxGrid) return NX_EUNSUPPORTED;
-  *out = {tile, n_rt, (n_wg + 7) / 8 * 8, blocks * kBlock * 2 * c->head_dim,
-          max_tokens <= (units >= kManyHeads && units <= kCUs ? kWholeMany : kWholeTokens)};
+  const int64_t whole = units >= kRounds ? (tile == 16 ? kWholeRounds : kWholeRounds / 4)
+                        : units >= kManyHeads && units <= kCUs ? kWholeMany : kWholeTokens;
+  *out = {tile, n_rt, (n_wg + 7) / 8 * 8, blocks * kBlock * 2 * c->head_dim, max_tokens <= whole};
   return NX_OK;
 }
 // Workspace: status word, the heads' pieces, partials.

@@ -714,3 +714,20 @@ def test_a_long_prompt_equals_its_parts():
         amax = torch.nn.functional.pad(x, (0, 0, 0, -n % 32)).view(hk, -1, 32 * d).abs().amax(-1)
         bound = (amax / 254 * (1 + 2.0 ** -20)).repeat_interleave(32, 1)[:, :n, None] + x.abs() * 2.0 ** -7
         assert ((y[0].float() - x).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("m", [1, 20])
+def test_a_thousand_heads(m):
+    """Whole heads by the number of heads, at a bound on the lengths that would cut fewer into pieces."""
+    S, most = 520, 2000
+    cache = Cache(S, 2, 2, 64, "bf16", "int8", 2, 4, max_q=m)
+    cache.fill([(53 * i) % 201 if i % 9 else 0 for i in range(2 * S)], garbage=False)
+    q = _randn(97, S * m, 4, 64, dtype="bf16")
+    ws = nx.new_paged_workspace(cache.cfg, cache.c, most, m)
+    lse = torch.empty(S * m, 4, device=DEV)
+    out = nx.nx_paged_attn(cache.cfg, cache.c, q, workspace=ws, max_tokens=most, max_q=m, out_lse=lse)
+    nx.nx_read_device_status(cache.cfg, ws)
+    _check_attn(cache, q, [m] * S, out, lse)
+    longer = nx.new_paged_workspace(cache.cfg, cache.c, 40000, m)      # in pieces
+    out = nx.nx_paged_attn(cache.cfg, cache.c, q, workspace=longer, max_tokens=40000, max_q=m)
+    _check_attn(cache, q, [m] * S, out)
