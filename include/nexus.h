@@ -361,8 +361,8 @@ nx_status nx_read_device_status(const nx_desc* desc);
  * writes nothing, and nx_paged_attn reads page 0 in its place.  A call's pages
  * are distinct for the (sequence, head)s that it writes; pages that are only
  * read may be shared.  Outputs that overlap another array of the call are
- * refused (NX_EALIAS), also the small ones and the workspace.  Without rows a call
- * does nothing.  Calls that may run at the same time have workspaces of their own.
+ * refused (NX_EALIAS), also the small ones and the workspace.  A call of no rows is
+ * valid.  Calls that may run at the same time have workspaces of their own.
  * The per-stage profiler covers the eviction stages only.  With NX_DEBUG set these
  * calls are synchronous too.
  */
