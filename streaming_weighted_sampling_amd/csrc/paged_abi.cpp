@@ -184,15 +184,27 @@ size_t part_ml_bytes(const Cut& k) { return align256(size_t(2 * k.n_wg * k.n_rt 
 size_t cut_bytes(const nx_paged* c, const Cut& k) {
   return 256 + pieces_bytes(c) + part_ml_bytes(k) + size_t(2 * k.n_wg * k.n_rt * k.tile) * c->head_dim * sizeof(float);
 }
+// The most that calls of up to max_tokens rows and max_q queries take.  The rounding
+// of n_wg and the change of tile size make a call's bytes rise and fall with its
+// query rows, so every count is asked for, up to the 2 kCUs / 8 row tiles past
+// which n_wg is the constant 8 and bytes only rise.  (They never fall as
+// max_tokens rises.)
+size_t most_bytes(const nx_paged* c, int64_t max_tokens, int64_t max_q) {
+  Cut k;
+  if (make_cut(c, max_tokens, max_q, &k) != NX_OK) return 0;
+  size_t most = cut_bytes(c, k);
+  const int64_t rows = 2 * kCUs / 8 * 32, group = c->n_q_heads / c->n_kv_heads;
+  for (int64_t q = std::min(max_q, rows / group + 1); q > 0; --q)
+    if (make_cut(c, max_tokens, q, &k) == NX_OK) most = std::max(most, cut_bytes(c, k));
+  return most;
+}
 
 }  // namespace
 
 extern "C" {
 
 size_t nx_paged_workspace_bytes(const nx_paged* cache, int32_t max_tokens, int32_t max_q) {
-  Cut k;
-  if (check_shape(cache) != NX_OK || make_cut(cache, max_tokens, max_q, &k) != NX_OK) return 0;
-  return cut_bytes(cache, k);
+  return check_shape(cache) == NX_OK ? most_bytes(cache, max_tokens, max_q) : 0;
 }
 
 nx_status nx_qk_norm_rope(const nx_desc* desc, const nx_rope* rope, int32_t n_rows, const nx_rows* q,

@@ -243,3 +243,22 @@ def test_rope_table_holds_fp64_angles():
     i = torch.arange(4, dtype=torch.float64)
     a = torch.arange(100000, 100005, dtype=torch.float64)[:, None] * 100.0 ** (-i / 4)
     assert torch.allclose(t[:, :4], a.cos(), atol=1e-7) and torch.allclose(t[:, 4:], a.sin(), atol=1e-7)
+
+
+@pytest.mark.parametrize("hq,hkv", [(64, 8), (40, 8), (8, 8), (5, 1), (32, 1), (256, 1)])
+@pytest.mark.parametrize("tokens", [0, 100, 1500, 32768])
+def test_a_workspace_serves_every_smaller_call(lib, hq, hkv, tokens):
+    """The size never falls with max_q or max_tokens, and a call of fewer queries passes the check
+    (it has no rows, so nothing is launched)."""
+    for n_seqs in (1, 4, 200):
+        c = _cache(n_seqs=n_seqs, n_q_heads=hq, n_kv_heads=hkv)
+        sizes = [lib.nx_paged_workspace_bytes(c, tokens, m) for m in range(1, 200)]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+        assert sizes[-1] <= lib.nx_paged_workspace_bytes(c, tokens, 4096)
+        assert all(lib.nx_paged_workspace_bytes(c, t, 17) <= sizes[16] for t in (0, tokens // 3, tokens))
+        for most in (16, 64, 150):
+            c.workspace_bytes = sizes[most - 1]
+            for m in range(1, most + 1):
+                for t in (tokens // 2, tokens):
+                    assert lib.nx_paged_attn(c, _r(20, 1 << 16), _r(21, 1 << 16), 0, None, t, m, 0.0,
+                                             None) == _lib.NX_OK, (most, m, t)
