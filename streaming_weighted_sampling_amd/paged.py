@@ -5,7 +5,8 @@ Between two eviction events each new token is normed and rotated
 over it (nx_paged_attn); nx_paged_gather reads the rows back for the next event.
 The functions mirror include/nexus.h; shapes and the element type come from the
 NexusConfig of the eviction calls.  Work is enqueued on the current stream of
-the tensors' device (or the given stream).
+the tensors' device (or the given stream, on which outputs that are not given are
+made too; ordering that stream behind the inputs is the caller's).
 """
 
 import ctypes
@@ -62,6 +63,15 @@ def _stream(stream, index):
     if stream.device.index != index:
         raise ValueError(f"the stream is on {stream.device}, the tensors on GPU {index}")
     return stream.cuda_stream
+
+
+def _new(make, stream):
+    """A default output, made on the stream that the call runs on: its memory (and its fill)
+    belongs to that stream's order."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
 
 
 def _run(index, fn, *args):
@@ -207,13 +217,13 @@ def nx_qk_norm_rope(cfg, q, k=None, *, workspace, q_weight=None, k_weight=None, 
     dev, n, hq, hk, d = q.get_device(), q.shape[0], cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim
     rq = _rows(cfg, q, "q", hq, dev, n)
     if out_q is None:
-        out_q = torch.empty(n, hq, d, dtype=cfg.dtype, device=q.device)
+        out_q = _new(lambda: torch.empty(n, hq, d, dtype=cfg.dtype, device=q.device), stream)
     roq = _rows(cfg, out_q, "out_q", hq, dev, n)
     rk = rok = None
     if k is not None:
         rk = _rows(cfg, k, "k", hk, dev, n)
         if out_k is None:
-            out_k = torch.empty(n, hk, d, dtype=cfg.dtype, device=q.device)
+            out_k = _new(lambda: torch.empty(n, hk, d, dtype=cfg.dtype, device=q.device), stream)
         rok = _rows(cfg, out_k, "out_k", hk, dev, n)
     elif out_k is not None:
         raise ValueError("out_k without k")
@@ -273,7 +283,7 @@ def nx_paged_attn(cfg, cache, q, *, workspace, max_tokens, max_q=None, q_start=N
     dev, n, hq = cache._index, q.shape[0], cfg.n_q_heads
     rq = _rows(cfg, q, "q", hq, dev, n)
     if out is None:
-        out = torch.empty(n, hq, cfg.head_dim, dtype=cfg.dtype, device=q.device)
+        out = _new(lambda: torch.empty(n, hq, cfg.head_dim, dtype=cfg.dtype, device=q.device), stream)
     ro = _rows(cfg, out, "out", hq, dev, n)
     max_q = _per_seq(cache, n, max_q, q_start, "max_q", "q_start") if n else 1      # no rows: nothing is done
     if scale is not None and not scale > 0:
@@ -291,9 +301,9 @@ def nx_paged_gather(cfg, cache, *, workspace, max_tokens, out_k=None, out_v=None
     length are left as they were; new outputs are zero-filled); returns (out_k, out_v)."""
     shape, d = (cache.n_seqs, cfg.n_kv_heads, max_tokens, cfg.head_dim), cfg.head_dim
     if out_k is None:
-        out_k = torch.zeros(shape, dtype=cfg.dtype, device=cache.device)
+        out_k = _new(lambda: torch.zeros(shape, dtype=cfg.dtype, device=cache.device), stream)
     if out_v is None:
-        out_v = torch.zeros_like(out_k)
+        out_v = _new(lambda: torch.zeros_like(out_k), stream)
     for t, name in ((out_k, "out_k"), (out_v, "out_v")):
         got, st = t.shape, t.stride()
         if t.dtype is not cfg.dtype or len(got) != 4 or got[:2] != shape[:2] or got[2] < max_tokens or \

@@ -731,3 +731,25 @@ def test_a_thousand_heads(m):
     longer = nx.new_paged_workspace(cache.cfg, cache.c, 40000, m)      # in pieces
     out = nx.nx_paged_attn(cache.cfg, cache.c, q, workspace=longer, max_tokens=40000, max_q=m)
     _check_attn(cache, q, [m] * S, out)
+
+
+def test_default_outputs_on_a_side_stream():
+    """The current stream is kept busy while another stream's calls make their own outputs."""
+    cache = Cache(2, 2, 2, 128, "bf16", "e4m3", 4, 8)
+    cache.fill([1000, 33, 0, 640])
+    q, k = _randn(101, 2, 4, 128, dtype="bf16"), _randn(102, 2, 2, 128, dtype="bf16")
+    want = (nx.nx_qk_norm_rope(cache.cfg, q, k, workspace=cache.ws, q_weight=q[0, 0])[0],
+            nx.nx_paged_attn(cache.cfg, cache.c, q, workspace=cache.ws, max_tokens=1000),
+            *nx.nx_paged_gather(cache.cfg, cache.c, workspace=cache.ws, max_tokens=1000))
+    side, big = torch.cuda.Stream(), torch.randn(4096, 4096, device=DEV)
+    for _ in range(3):
+        torch.cuda.synchronize()
+        for _ in range(20):
+            big @ big
+        got = (nx.nx_qk_norm_rope(cache.cfg, q, k, workspace=cache.ws, q_weight=q[0, 0], stream=side)[0],
+               nx.nx_paged_attn(cache.cfg, cache.c, q, workspace=cache.ws, max_tokens=1000, stream=side),
+               *nx.nx_paged_gather(cache.cfg, cache.c, workspace=cache.ws, max_tokens=1000, stream=side))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del got
+    cache.check()

@@ -262,3 +262,39 @@ def test_a_workspace_serves_every_smaller_call(lib, hq, hkv, tokens):
                 for t in (tokens // 2, tokens):
                     assert lib.nx_paged_attn(c, _r(20, 1 << 16), _r(21, 1 << 16), 0, None, t, m, 0.0,
                                              None) == _lib.NX_OK, (most, m, t)
+
+
+def test_default_outputs_are_made_on_the_given_stream(monkeypatch):
+    """Memory made on one stream and written on another could still be in use there, and a fill on
+    the one could land on top of the other's result."""
+    import contextlib
+
+    from streaming_weighted_sampling_amd import paged
+    cfg = nx.NexusConfig(4, 2, 64, 1, torch.bfloat16)
+    c = nx.new_paged_cache(cfg, 3, 8, 2, device="cpu")
+    ws, q, k = torch.zeros(4096, dtype=torch.uint8), torch.zeros(3, 4, 64).bfloat16(), torch.zeros(3, 2, 64).bfloat16()
+    current, made = [None], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        current.append(stream)
+        yield
+        current.pop()
+
+    def noting(make):
+        def f(*a, **kw):
+            made.append(current[-1])
+            return make(*a, **kw)
+        return f
+
+    monkeypatch.setattr(paged, "_run", lambda *a: 0)
+    monkeypatch.setattr(paged, "_stream", lambda *a: None)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    for name in ("empty", "zeros", "zeros_like"):
+        monkeypatch.setattr(torch, name, noting(getattr(torch, name)))
+    for stream in (None, "side"):
+        nx.nx_qk_norm_rope(cfg, q, k, workspace=ws, stream=stream)
+        nx.nx_paged_attn(cfg, c, q, workspace=ws, max_tokens=4, stream=stream)
+        nx.nx_paged_gather(cfg, c, workspace=ws, max_tokens=4, stream=stream)
+        assert made == [stream] * 5
+        made.clear()
