@@ -13,7 +13,7 @@ moves inside libnexus.so.
 
 import torch
 
-from ._lib import NX_CACHE_BLOCK, NX_HEADS_UNIFORM
+from ._lib import NX_CACHE_BLOCK, NX_HEADS_ALLOC, NX_HEADS_UNIFORM, NexusError
 from .api import NexusConfig, make_units, new_workspace, nx_evict_batch, nx_read_device_status
 from .paged import (new_paged_cache, new_paged_workspace, nx_paged_append, nx_paged_attn, nx_paged_gather,
                     nx_qk_norm_rope)
@@ -101,7 +101,8 @@ class DecodeCache:
         return nx_paged_attn(cfg, self.cache, q_rot, workspace=self.ws, max_tokens=self.rows, out=self.out)
 
     def evict(self):
-        """One eviction event over all sequences, back to the budget."""
+        """One eviction event over all sequences, back to the budget.  A head that the device rejects
+        (check() raises) keeps all its rows."""
         cfg, w = self.cfg, self.cfg.window
         if self.queries < w:
             raise ValueError(f"an event needs {w} queries, {self.queries} were seen")
@@ -123,15 +124,32 @@ class DecodeCache:
                       head_cap=self.head_cap, head_budget=self.head_budget[s],
                       head_tokens=self.cache.lens[s], head_tokens_out=self.counts[s])
                  for s in range(self.n_seqs)], device=self.device)
+        # The event writes the count of every head that it serves; one that the device rejects keeps -1
+        # here, and its rows as they were.
+        self.counts.fill_(-1)
+        if cfg.head_alloc == NX_HEADS_ALLOC:
+            self.head_budget.fill_(-1)
         nx_evict_batch(cfg, units, self.n_seqs, self.rows, self.walk_iters, self.seed, workspace=self.evict_ws,
                        step=self.step_no, max_out_rows=kept)
-        self.cache.lens.zero_()
+        if cfg.head_alloc == NX_HEADS_ALLOC and cfg.n_sink + cfg.n_recent == 0:
+            # An allocation of no rows is not rejected (no row is forced): such a head keeps none.
+            self.counts.masked_fill_((self.counts < 0) & (self.head_budget == 0) & (self.cache.lens <= self.rows), 0)
+        self.cache.lens.masked_fill_(self.counts >= 0, 0)
+        self.counts.clamp_(min=0)
         nx_paged_append(cfg, self.cache, self.kept_k.permute(1, 0, 2), self.kept_v.permute(1, 0, 2),
                         workspace=self.ws, max_new=self.cap_rows, head_new=self.counts)
         self.rows = kept
         self.step_no += 1
 
     def check(self):
-        """Synchronises and raises NexusError on an error that a step or an event recorded."""
-        nx_read_device_status(self.cfg, self.ws)
-        nx_read_device_status(self.cfg, self.evict_ws)
+        """Synchronises and raises NexusError on an error that a step or an event recorded (both are
+        cleared).  The cache can be used on: what was rejected is as it was before."""
+        errors = []
+        for ws in (self.ws, self.evict_ws):
+            try:
+                nx_read_device_status(self.cfg, ws)
+            except NexusError as e:
+                errors.append(e)
+        if errors:
+            self.rows = max(0, int(self.cache.lens.max()))     # a rejected head may be longer than the bound
+            raise errors[0]

@@ -122,3 +122,74 @@ def test_decode_cache_refuses_what_it_cannot_hold():
                             device=DEV)
     with pytest.raises(ValueError, match="positions"):
         turned.step(q, k, k)
+
+
+def _held(dec, s, h):
+    """What the cache holds of one head: the rows it stands for and the unquantised ones."""
+    k, v = nx.nx_paged_gather(dec.cfg, dec.cache, workspace=dec.ws, max_tokens=dec.capacity)
+    n = int(dec.cache.lens[s, h])
+    return n, k[s, h, :n].clone(), v[s, h, :n].clone()
+
+
+def _fill(dec, rows, steps, seed=200):
+    S, hk, hq, d = dec.n_seqs, dec.cfg.n_kv_heads, dec.cfg.n_q_heads, dec.cfg.head_dim
+    dec.load(_randn(seed, S, hk, rows, d, dtype="bf16"), _randn(seed + 1, S, hk, rows, d, dtype="bf16"))
+    for i in range(steps):
+        qkv = _randn(seed + 2 + i, S, hq + 2 * hk, d, dtype="bf16")
+        dec.step(*qkv.split((hq, hk, hk), 1))
+
+
+@pytest.mark.parametrize("events", [0, 1])
+def test_a_rejected_head_keeps_its_rows(events):
+    """One head's resident count is out of range for the event (in the first event, and in one after
+    which the buffers hold an earlier event's rows)."""
+    cfg = nx.NexusConfig(4, 2, 64, 4)
+    dec = nx.DecodeCache(cfg, 2, 256, 50, 2, page_blocks=2, device=DEV)
+    _fill(dec, 90, 10)
+    for _ in range(events):
+        dec.evict()
+        _fill(dec, 120, 7, seed=300)
+    dec.check()
+    n = dec.rows
+    dec.rows -= 3                              # the host's bound is too low for every head ...
+    dec.cache.lens[0].sub_(3)                  # ... but those of sequence 0, which now hold three fewer
+    before = [_held(dec, s, h) for s in range(2) for h in range(2)]
+    dec.evict()
+    with pytest.raises(nx.NexusError) as e:
+        dec.check()
+    assert e.value.code == nx.NX_EINVAL
+    assert dec.cache.lens.tolist() == [[50, 50], [n, n]] and dec.rows == n
+    for h in range(2):
+        got = _held(dec, 1, h)
+        assert got[0] == n and all(torch.equal(a, b) for a, b in zip(got[1:], before[2 + h][1:]))
+    dec.check()
+    _fill_more = _randn(400, 2, 8, 64, dtype="bf16").split((4, 2, 2), 1)
+    dec.step(*_fill_more)
+    dec.evict()                                # with the bound put right the same heads are served
+    dec.check()
+    assert dec.cache.lens.tolist() == [[50, 50], [50, 50]]
+
+
+def test_a_head_that_is_allocated_no_rows_is_empty():
+    """Head 0 attends evenly over 100 rows, head 1 over 20 only, whose weights are then the 20 largest
+    of both heads: two heads of budget 10 leave nothing for head 0."""
+    cfg = nx.NexusConfig(2, 2, 64, 4, head_alloc=2, head_floor=0)
+    dec = nx.DecodeCache(cfg, 1, 128, 10, 0, page_blocks=1, head_cap=40, device=DEV)
+    k = torch.zeros(1, 2, 96, 64, dtype=torch.bfloat16, device=DEV)
+    k[0, 1, :, 0] = -8.0
+    k[0, 1, 5:25, 0] = 8.0
+    v = _randn(1, 1, 2, 96, 64, dtype="bf16")
+    dec.load(k, v)
+    q = torch.zeros(1, 2, 64, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 8.0
+    new = torch.zeros(1, 2, 64, dtype=torch.bfloat16, device=DEV)
+    new[0, 1, 0] = -8.0
+    for _ in range(4):
+        dec.step(q, new, new)
+    dec.evict()
+    dec.check()
+    assert dec.head_budget.tolist() == [[0, 20]] and dec.cache.lens.tolist() == [[0, 20]]
+    assert dec.keep[0, 1, :20].tolist() == list(range(5, 25))
+    out = dec.step(q, new, new)
+    dec.check()
+    assert torch.equal(out[0, 0], new[0, 0]) and dec.cache.lens.tolist() == [[1, 21]]
