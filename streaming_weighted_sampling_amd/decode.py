@@ -13,7 +13,7 @@ moves inside libnexus.so.
 
 import torch
 
-from ._lib import NX_CACHE_BLOCK, NX_HEADS_ALLOC, NX_HEADS_UNIFORM, NexusError
+from ._lib import NX_CACHE_BLOCK, NX_HEADS_ALLOC, NX_HEADS_GIVEN, NX_HEADS_UNIFORM, NexusError
 from .api import NexusConfig, make_units, new_workspace, nx_evict_batch, nx_read_device_status
 from .paged import (new_paged_cache, new_paged_workspace, nx_paged_append, nx_paged_attn, nx_paged_gather,
                     nx_qk_norm_rope)
@@ -23,6 +23,9 @@ class DecodeCache:
     """`n_seqs` sequences of one layer, up to `capacity` rows per head.
 
     rope: Rope or None; q_weight / k_weight: [head_dim] norm weights or None.
+    head_budget: with head_alloc = NX_HEADS_GIVEN the units that each head keeps, [n_seqs, n_kv_heads]
+    or what expands to it, at most head_cap (0: budget); the attribute, int32 on the device, may be
+    rewritten in place between events.
     Keys are rotated (and normed) once, when they arrive; evicted positions
     leave holes that nothing refers to again, so a kept row is stored as it was.
     Evicting re-quantises the kept rows in their new blocks.  With cfg.block > 1 an
@@ -30,9 +33,12 @@ class DecodeCache:
     """
 
     def __init__(self, cfg: NexusConfig, n_seqs, capacity, budget, walk_iters, *, fmt="e4m3", page_blocks=4,
-                 rope=None, q_weight=None, k_weight=None, eps=1e-6, seed=0, layer=0, head_cap=0, device="cuda"):
+                 rope=None, q_weight=None, k_weight=None, eps=1e-6, seed=0, layer=0, head_cap=0, head_budget=None,
+                 device="cuda"):
         if cfg.compact:
             raise ValueError("the kept rows are copied into new blocks: compact must be 0")
+        if (cfg.head_alloc == NX_HEADS_GIVEN) != (head_budget is not None):
+            raise ValueError("head_budget goes with head_alloc = NX_HEADS_GIVEN")
         self.cfg, self.n_seqs, self.capacity = cfg, n_seqs, capacity
         self.budget, self.walk_iters, self.seed, self.layer = budget, walk_iters, seed, layer
         self.rope, self.q_weight, self.k_weight, self.eps = rope, q_weight, k_weight, eps
@@ -58,6 +64,13 @@ class DecodeCache:
         self.kept_v = torch.zeros_like(self.kept_k)
         self.keep = torch.zeros(n_seqs, hk, cap, dtype=torch.int32, device=self.device)
         self.head_budget = torch.zeros(n_seqs, hk, dtype=torch.int32, device=self.device)
+        if head_budget is not None:
+            given = torch.as_tensor(head_budget).expand(n_seqs, hk)
+            if given.is_floating_point() or int(given.min()) < max(1, cfg.n_sink + cfg.n_recent) or \
+                    int(given.max()) > cap:
+                raise ValueError(f"head_budget: whole numbers from {max(1, cfg.n_sink + cfg.n_recent)} (the forced "
+                                 f"units) to {cap} expected")
+            self.head_budget.copy_(given)
         self.counts = torch.zeros(n_seqs, hk, dtype=torch.int32, device=self.device)
         self.window = torch.zeros_like(self.ring)
         self.evict_ws = new_workspace(cfg, capacity, n_seqs, walk_iters, device=self.device)

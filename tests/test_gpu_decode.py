@@ -193,3 +193,23 @@ def test_a_head_that_is_allocated_no_rows_is_empty():
     out = dec.step(q, new, new)
     dec.check()
     assert torch.equal(out[0, 0], new[0, 0]) and dec.cache.lens.tolist() == [[1, 21]]
+
+
+def test_given_head_budgets():
+    cfg = nx.NexusConfig(4, 2, 64, 4, head_alloc=nx.NX_HEADS_GIVEN, n_sink=2)
+    given = torch.tensor([[30, 61], [7, 2]])
+    dec = nx.DecodeCache(cfg, 2, 256, 40, 2, page_blocks=2, head_cap=64, head_budget=given, device=DEV)
+    for _ in range(2):
+        _fill(dec, 100, 6)
+        dec.evict()
+        dec.check()
+        assert dec.cache.lens.tolist() == given.tolist() and dec.rows == 64
+        assert (dec.keep[:, :, :2] == torch.arange(2, device=DEV)).all()       # the forced units
+    dec.head_budget[0, 1] = 0                  # a budget that the event refuses
+    _fill(dec, 100, 6)
+    dec.evict()
+    with pytest.raises(nx.NexusError):
+        dec.check()
+    assert dec.cache.lens.tolist() == [[30, 106], [7, 2]] and dec.rows == 106
+    even = nx.DecodeCache(cfg, 2, 256, 40, 2, head_budget=[9, 40], device=DEV)
+    assert even.head_budget.tolist() == [[9, 40]] * 2

@@ -298,3 +298,19 @@ def test_default_outputs_are_made_on_the_given_stream(monkeypatch):
         nx.nx_paged_gather(cfg, c, workspace=ws, max_tokens=4, stream=stream)
         assert made == [stream] * 5
         made.clear()
+
+
+def test_given_head_budgets_are_asked_for_and_checked(lib):
+    def dec(alloc=nx.NX_HEADS_GIVEN, n_sink=0, **kw):
+        cfg = nx.NexusConfig(4, 2, 64, 4, head_alloc=alloc, n_sink=n_sink)
+        return nx.DecodeCache(cfg, 3, 256, 40, 2, device="cpu", **kw)
+    with pytest.raises(ValueError, match="head_budget"):
+        dec()
+    with pytest.raises(ValueError, match="head_budget"):
+        dec(nx.NX_HEADS_UNIFORM, head_budget=[9, 9])
+    for bad in ([0, 9], [9, 41], [-1, 9], [9.5, 9.0]):
+        with pytest.raises(ValueError, match="head_budget"):
+            dec(head_budget=bad)
+    with pytest.raises(ValueError, match="from 3 "):
+        dec(n_sink=3, head_budget=[2, 9])
+    assert dec(head_budget=[9, 60], head_cap=64).head_budget.tolist() == [[9, 60]] * 3
