@@ -7,7 +7,8 @@ again whenever the budget is hit.  This driver holds the kept rows in the paged
 attends; evict() reads the cache back, runs one nx_evict_batch event over all
 sequences with the last W queries as the window, and refills the cache with the
 kept rows.  Nothing synchronises: row counts, also the heads' different ones under
-per-head budgets, stay on the device.  Marshalling only; every byte of a step
+per-head budgets, stay on the device (but for an event at full capacity whose head_cap
+is the capacity too: the next steps then need the counts).  Marshalling only; every byte of a step
 moves inside libnexus.so.
 """
 
@@ -115,17 +116,20 @@ class DecodeCache:
 
     def evict(self):
         """One eviction event over all sequences, back to the budget.  A head that the device rejects
-        (check() raises) keeps all its rows."""
+        (check() raises) keeps all its rows.  A budget of the whole capacity is refused once the cache is
+        full: nothing could follow."""
         cfg, w = self.cfg, self.cfg.window
         if self.queries < w:
             raise ValueError(f"an event needs {w} queries, {self.queries} were seen")
         if self.rows % cfg.block:     # a short last block would be counted as a whole one
             raise ValueError(f"{self.rows} rows are not whole blocks of {cfg.block}")
+        kept = min(cfg.kept_rows(self.rows, self.head_cap), self.cap_rows)
+        if kept == self.capacity and cfg.head_alloc == NX_HEADS_UNIFORM:
+            raise ValueError(f"an event makes no room: its budget holds all {self.capacity} rows of the capacity")
         first = self.queries % w                 # the oldest query's place in the ring
         self.window[:, :, :w - first].copy_(self.ring[:, :, first:])
         self.window[:, :, w - first:].copy_(self.ring[:, :, :first])
         nx_paged_gather(cfg, self.cache, workspace=self.ws, max_tokens=self.rows, out_k=self.k, out_v=self.v)
-        kept = min(cfg.kept_rows(self.rows, self.head_cap), self.cap_rows)
         units = self._units.get(self.rows)
         if units is None:
             d, r = cfg.head_dim, self.cap_rows
@@ -151,7 +155,8 @@ class DecodeCache:
         self.counts.clamp_(min=0)
         nx_paged_append(cfg, self.cache, self.kept_k.permute(1, 0, 2), self.kept_v.permute(1, 0, 2),
                         workspace=self.ws, max_new=self.cap_rows, head_new=self.counts)
-        self.rows = kept
+        # Where a head may keep as many rows as the cache holds, only the counts say how long the longest is.
+        self.rows = kept if kept < self.capacity else max(0, int(self.cache.lens.max()))
         self.step_no += 1
 
     def check(self):

@@ -213,3 +213,32 @@ def test_given_head_budgets():
     assert dec.cache.lens.tolist() == [[30, 106], [7, 2]] and dec.rows == 106
     even = nx.DecodeCache(cfg, 2, 256, 40, 2, head_budget=[9, 40], device=DEV)
     assert even.head_budget.tolist() == [[9, 40]] * 2
+
+
+def test_events_under_a_head_cap_of_the_whole_capacity():
+    """The loop "step until full, then evict" goes on: the bound on the rows follows the heads' counts."""
+    cfg = nx.NexusConfig(4, 2, 64, 4, head_alloc=2, head_floor=8)
+    dec = nx.DecodeCache(cfg, 2, 64, 24, 2, page_blocks=1, head_cap=64, device=DEV)
+    _fill(dec, 50, 0)
+    for event in range(3):
+        while dec.rows < dec.capacity:
+            dec.step(*_randn(500 + dec.rows, 2, 8, 64, dtype="bf16").split((4, 2, 2), 1))
+        dec.evict()
+        dec.check()
+        lens = dec.cache.lens
+        assert dec.rows == int(lens.max()) < 64 and (lens.sum(1) == 48).all()
+
+
+def test_an_event_that_makes_no_room_is_refused():
+    dec = nx.DecodeCache(nx.NexusConfig(4, 2, 64, 4), 1, 64, 64, 2, page_blocks=1, device=DEV)
+    _fill(dec, 50, 10)
+    before = _held(dec, 0, 1)
+    dec.evict()                                # below the capacity: keeps every row, quantised anew
+    dec.check()
+    assert dec.rows == 60 and _held(dec, 0, 1)[0] == before[0] == 60
+    _fill(dec, 60, 4)
+    before = _held(dec, 0, 1)
+    with pytest.raises(ValueError, match="room"):
+        dec.evict()
+    dec.check()
+    assert dec.step_no == 1 and all(torch.equal(a, b) for a, b in zip(_held(dec, 0, 1)[1:], before[1:]))
