@@ -473,6 +473,12 @@ nx_status nx_paged_append(const nx_paged* cache, const nx_rope* rope, const nx_r
  *   scale      factor of q . k; 0: 1 / sqrt(head_dim)
  *   out_lse    nullable [n_rows][n_q_heads] fp32: ln of the sum of exp(scale q . k)
  * The result does not depend on the order in which workgroups run.
+ * Weights are fp32 and enter the product with V exact to 2^-11 (NX_BF16) or 2^-22
+ * (NX_F32) of themselves, however far apart the scales of V's blocks lie (a block
+ * below 2^-80 of the head's largest counts as if it were at 2^-80); where a head's
+ * scales all lie within 2^14 (NX_BF16) or 2^8 (NX_F32) of each other a further 2^-18
+ * or 2^-24 of each block's largest |v| may be lost for each row.  The cached rows
+ * times the largest |v| must stay below 2^110.
  */
 nx_status nx_paged_attn(const nx_paged* cache, const nx_rows* q, const nx_rows* out, int32_t n_rows,
                         const int32_t* q_start, int32_t max_tokens, int32_t max_q, float scale,

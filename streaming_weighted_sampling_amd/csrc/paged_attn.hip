@@ -35,7 +35,11 @@
 // row's largest and off by at most 2^-38 of it below, fp32 rows use a second f16
 // term for the remainder (22 bits).
 // p enters as f16 (relative 2^-11, against the bf16 result's 2^-8), or as two
-// f16 terms for fp32 rows.  Sums, references and accumulators are fp32.
+// f16 terms for fp32 rows, with its block's V scale over the wavefront's reference
+// scale in it.  f16's smallest step bounds how far below the largest p a product
+// with a large |v| may still count, so where a wavefront's V scales lie far apart
+// (kNear) what f16 leaves of a small p enters too, scaled up, in further products.
+// Sums, references and accumulators are fp32.
 #include "paged.hpp"
 
 namespace nx {
@@ -44,13 +48,29 @@ namespace {
 constexpr float kNoBase = 1e30f;     // base of a row that has seen nothing
 constexpr float kNoScale = -200.f;   // log2 of V's reference before the first block
 // p is held times 2^7 at its row's reference and may grow by 2^7 (times V's
-// scale ratio, at most 2) before the reference moves: f16 values stay below 2^15.
+// scale ratio, at most 2) before the reference moves: f16 values stay below 2^16.
 constexpr float kHead = 7.f;
-// V's scale ratio is taken as at least 2^-40: times p, at most 2^14, that is
-// below half of f16's smallest step, so such a block adds nothing to o.  In
-// general o is exact to 2^-31 of the head's largest |v| for each row, from
-// f16's smallest step.  (The tail's p is not held in f16.)
-constexpr float kLeast = -40.f, kLeastTail = -80.f;
+// A wavefront keeps p in f16 while the scales of the V blocks that it has met lie
+// within 2^kNear of the first one's, so within w = 2 kNear of each other: half of
+// f16's smallest step is 2^-25, the sum of p at least 2^7, so o is exact to
+// n 2^(w - 32) of the weighted mean of each block's largest |v| (n cached rows).
+// (Normally distributed values: within 2^1.)
+template <bool kF32> constexpr float kNear = kF32 ? 4.f : 7.f;
+// Where they do not, what f16 left of the p below kBelow (at most 2^-25) is scaled
+// by kStep, o with it, and enters as f16 again, kRounds times: up by 2^72 in all and
+// exact to 2^-97 then, where the largest p of a block of the least ratio is 2^-73.
+// (From kBelow on p is exact to 2^-11, its two terms to 2^-22.)  o stays below 2^48
+// (2^15 times a code times 2^24 rows), scaled up below 2^120.
+// Rare, so made small and not fast (scales alternating by 2^20: 16 heads of 131077
+// rows 93 -> 141 us, 64 queries of 8 heads in groups of 8 over 32768 rows 94 -> 255).
+template <bool kF32> struct Rest {
+  static constexpr int kRounds = kF32 ? 4 : 3;
+  static constexpr float kBelow = kF32 ? 0x1p-3f : 0x1p-14f, kStep = kF32 ? 0x1p18f : 0x1p24f;
+};
+// V's scale ratio counts as at least 2^kLeast, which is 2^-80 of the head's
+// largest |v|.  A block of scale 0 has its p held 2^40 lower, at most 2^-26: less
+// than half of f16's smallest step, so whatever its codes are they add nothing.
+constexpr float kLeast = -80.f, kLeastZero = -40.f;
 
 template <int kFmt>
 __device__ inline h8_t codes_f16(uint32_t lo, uint32_t hi) {
@@ -205,13 +225,13 @@ __device__ inline float lane_of(float x, int i) {
 
 // The exponents z of one block's p from its products s (-infinity: hidden),
 // with the block's V scale vs over the reference in them; moves references.
-// t[rt] > 0: factor to log2 units; lvs: log2(vs); the ratio counts as at least
-// 2^least.  Returns the power that the sum of p takes out again (log2 of the
-// ratio is good to 2^-20, the sum sees the same value).
+// t[rt] > 0: factor to log2 units; lvs: log2(vs).  Returns the power that the sum
+// of p takes out again (log2 of the ratio is good to 2^-18, the sum sees the same
+// value).
 template <int D, int RT>
 __device__ inline float exponents(State<D, RT>& st, const f32x4_t (&s)[RT][2], const float (&t)[RT], float vs,
-                                  float lvs, float least, float (&z)[RT][8]) {
-  float shift = fmaxf(lvs - st.lvref, least);
+                                  float lvs, float (&z)[RT][8]) {
+  float shift = fmaxf(lvs - st.lvref, vs > 0.f ? kLeast : kLeastZero);
   float top = -__builtin_inff();
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
@@ -222,7 +242,7 @@ __device__ inline float exponents(State<D, RT>& st, const f32x4_t (&s)[RT][2], c
       top = fmaxf(top, z[rt][e]);
     }
   }
-  if (__any(top > 2.f * kHead) || shift > 1.f) {
+  if (__any(top > 2.f * kHead + shift) || shift > 1.f) {   // (p itself, without the ratio)
     // Rare: a row's reference moves to its largest logit so far, or V's
     // reference scale to this block's; what is accumulated follows.
     float f = 1.f;
@@ -285,7 +305,7 @@ __device__ inline void write_lse(const PagedArgs& a, const Job& job, int h, int 
 // whole, for calls of short heads, which then need neither the search for the
 // piece nor the merge launch.
 template <int D, bool kF32, int kFmt, int RT, bool kNT, bool kWhole, int kWaves>
-__global__ __launch_bounds__(64 * kWaves) void attn_kernel(PagedArgs a) {
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_kernel(PagedArgs a) {
   using E = Elem<kF32>;
   constexpr int kC = D / 32;          // 32-element chunks of a row
   constexpr int NP = kF32 ? 2 : 1;    // f16 terms of q and p
@@ -374,6 +394,31 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(PagedArgs a) {
 #pragma unroll
     for (int n = 0; n < kVL; ++n) vr[n] = vb.ld16<kNT ? kNonTemporal : 0>((g * D + 2 * c16) * 8 + 256 * n);
   };
+  // V's first scale (log2), and whether another lies further from it than kNear.
+  float lv_first = kNoScale;
+  bool far_apart = false;
+  // fp32 rows in two tiles leave no registers for p until its rest is known to be
+  // needed: it waits in this wavefront's part of so.
+  constexpr bool kParked = kF32 && RT == 2;
+  auto park = [&](const float (&x)[RT][8]) {
+#pragma unroll
+    for (int i = 0; i < 2 * RT; ++i)
+      so[wave][i][lane] = f32x4_t{x[i / 2][i % 2 * 4], x[i / 2][i % 2 * 4 + 1], x[i / 2][i % 2 * 4 + 2], x[i / 2][i % 2 * 4 + 3]};
+  };
+  auto fetch = [&](float (&x)[RT][8]) {
+#pragma unroll
+    for (int i = 0; i < 8 * RT; ++i) x[i / 8][i % 8] = so[wave][i / 4][lane][i % 4];
+  };
+  auto to_f16 = [](const float (&x)[RT][8], h8_t (&y)[RT][NP]) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const _Float16 hi = _Float16(x[rt][e]);
+        y[rt][0][e] = hi;
+        if constexpr (kF32) y[rt][NP - 1][e] = _Float16(x[rt][e] - float(hi));
+      }
+  };
   // The first block is on its way while q is prepared.
   if (w0 < wf) {
     look_up(w0);
@@ -421,6 +466,10 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(PagedArgs a) {
       load_v(0);
     }
     const float lvs_l = vs_l > 0.f ? log2f(vs_l) : kNoScale * 4.f;
+    // Lanes without a block have scale 0.
+    const uint64_t live = __ballot(vs_l > 0.f);
+    if (lv_first == kNoScale && live != 0) lv_first = lane_of(lvs_l, __builtin_ctzll(live));
+    if (__any(vs_l > 0.f && fabsf(lvs_l - lv_first) > kNear<kF32>)) far_apart = true;
     f32x4_t s[RT][2];
     auto products = [&] {   // s = K q^T of the block in kr
 #pragma unroll
@@ -453,17 +502,11 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(PagedArgs a) {
           for (int e = 0; e < 8; ++e)
             if (t0 + 8 * g + e > seen[rt]) s[rt][e / 4][e % 4] = -__builtin_inff();
       }
-      const float back = exponents<D, RT>(st, s, t, vs, lvs, kLeast, z);
+      const float back = exponents<D, RT>(st, s, t, vs, lvs, z);
       exponentiate<D, RT>(st, back, z);
+      if constexpr (kParked) park(z);
       h8_t pp[RT][NP];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const _Float16 hi = _Float16(z[rt][e]);
-          pp[rt][0][e] = hi;
-          if constexpr (kF32) pp[rt][NP - 1][e] = _Float16(z[rt][e] - float(hi));
-        }
+      to_f16(z, pp);
 #pragma unroll
       for (int n = 0; n < kVL; ++n)
 #pragma unroll
@@ -476,6 +519,50 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(PagedArgs a) {
               st.o[rt][2 * n + u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, pp[rt][np],
                                                                          st.o[rt][2 * n + u], 0, 0, 0);
         }
+      if (__builtin_expect(far_apart && vs > 0.f, 0)) {
+#pragma unroll 1
+        for (int round = 0; round < Rest<kF32>::kRounds; ++round) {
+          if constexpr (kParked) fetch(z);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[rt][e] = fabsf(z[rt][e]) < Rest<kF32>::kBelow ? z[rt][e] : 0.f;
+          h8_t pr[RT][NP];
+          to_f16(z, pr);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              z[rt][e] -= float(pr[rt][0][e]);
+              if constexpr (kF32) z[rt][e] -= float(pr[rt][NP - 1][e]);
+              z[rt][e] *= Rest<kF32>::kStep;
+            }
+          if constexpr (kParked) park(z);
+          to_f16(z, pr);
+#pragma unroll
+          for (int n = 0; n < kVL; ++n)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              // Converted anew, a few at a time: there are no registers to keep them in.
+              __builtin_amdgcn_sched_barrier(0);
+              uint32_t lo = u ? vr[n].z : vr[n].x, hi = u ? vr[n].w : vr[n].y;
+              asm volatile("" : "+v"(lo), "+v"(hi));
+              const h8_t v8 = codes_f16<kFmt>(lo, hi);
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt) {
+                st.o[rt][2 * n + u] *= Rest<kF32>::kStep;
+#pragma unroll
+                for (int np = 0; np < NP; ++np)
+                  st.o[rt][2 * n + u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, pr[rt][np],
+                                                                             st.o[rt][2 * n + u], 0, 0, 0);
+              }
+            }
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n) st.o[rt][n] *= 0x1p-72f;
+      }
       if (i + 1 < n8) load_v(i + 1);
     }
   }
@@ -528,7 +615,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(PagedArgs a) {
         if (8 * g + e >= nt || full * kBlock + 8 * g + e > seen[rt]) s[rt][e / 4][e % 4] = -__builtin_inff();
     }
     float p[RT][8];
-    exponentiate<D, RT>(st, exponents<D, RT>(st, s, t, 1.f, 0.f, kLeastTail, p), p);
+    exponentiate<D, RT>(st, exponents<D, RT>(st, s, t, 1.f, 0.f, p), p);
 #pragma unroll
     for (int n = 0; n < D / 32; ++n)
 #pragma unroll

@@ -753,3 +753,64 @@ def test_default_outputs_on_a_side_stream():
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         del got
     cache.check()
+
+
+# V's scale by block, in powers of two, of 25 blocks and a head whose scales reach up to 2^k
+V_SCALES = {
+    "alternate": lambda b, k: k * (b % 2), "small_first": lambda b, k: k * (b % 8 > 3),
+    "large_first": lambda b, k: k * (b % 8 < 4), "stairs": lambda b, k: k * (b % 5) / 4,
+    "one_large": lambda b, k: k * (b == 11)}
+
+
+def _far_scales_cache(dtype, fmt, d, k, order, max_q):
+    """Keys of +-1 in element 0 (+1 where V's scale is the small one, and in the tail), so that a query's
+    element 0 alone says how the weights split between blocks of small and of large V."""
+    cache = Cache(1, 1, 4, d, dtype, fmt, 2, 14, max_q=max_q)
+    cache.fill([25 * 32 + 9], seed=6)
+    c, top = cache.c, float(paged.TOP[fmt])
+    c.k_codes.view(torch.uint8).zero_()
+    c.k_tail.zero_()
+    c.k_tail[..., 0] = 1.0
+    rng = np.random.default_rng(5)
+    for b in range(25):
+        page, at = int(c.table[0, 0, b // 2]), b % 2
+        e = V_SCALES[order](b, k)
+        c.k_codes[page, at, :, 0] = torch.full((32,), top if e == 0 else -top).to(c.k_codes.dtype)
+        c.k_scale[page, at] = 1.0 / top
+        c.v_scale[page, at] = 2.0 ** e * (1.0 + rng.random()) / 2 / top
+    c.v_scale[int(c.table[0, 0, 3]), 0] = 0.0          # codes that stand for zeros
+    return cache
+
+
+@pytest.mark.parametrize("order", list(V_SCALES))
+@pytest.mark.parametrize("dtype,fmt,d", [("f32", "int8", 64), ("f32", "e4m3", 128), ("bf16", "e4m3", 64),
+                                         ("bf16", "int8", 128)])
+@pytest.mark.parametrize("k", [0, 10, 20, 30, 60])
+def test_attention_over_v_scales_far_apart(k, dtype, fmt, d, order):
+    """Each output against the bound of _attn_bound with its last term (p's smallest f16 step, against the
+    head's largest |v|) replaced: where a wavefront's V scales lie within 2^w of each other (w = 8 for fp32
+    rows, 14 for bf16 ones), p's half step 2^-25 times the reference scale is, against the sum of p of at
+    least 2^7, n 2^(w - 32) of the weighted mean of each block's largest |v|; where they do not, p's rest
+    enters as well, and a p is exact to 2^-11 and 2^-22 but for 2^-97 against a largest p of 2^(7 - 73) at
+    this test's ratios (2^61 and the tail's) and more, far below the former."""
+    w = 8 if dtype == "f32" else 14
+    for m in (1, 6):
+        cache = _far_scales_cache(dtype, fmt, d, k, order, 6)
+        q = torch.zeros(m, 4, d, dtype=DT[dtype], device=DEV)
+        # log2 of the weight of a small-V row over that of a large-V one: even, all small, balanced, all large
+        lg = torch.tensor([0.0, 100.0, float(k), -100.0])
+        q[:, :, 0] = (lg * 0.34657359).to(DEV) * torch.linspace(1, 0.9, m, device=DEV)[:, None]
+        kk, v = cache.rows(0, 0)
+        largest = np.abs(v).max(-1)
+        for b in range(25):
+            largest[32 * b:32 * b + 32] = np.abs(v[32 * b:32 * b + 32]).max()
+        o, _, mag, size = paged.attend(_np(q), kk, v, 1.0)
+        mean = paged.attend(_np(q), kk, largest[:, None], 1.0)[0]
+        bound = _attn_bound(dtype, d, o, mag, size, v[:0]) + len(v) * 2.0 ** (w - 32) * mean
+        for most in (809, 100000):
+            ws = nx.new_paged_workspace(cache.cfg, cache.c, most, m)
+            out = nx.nx_paged_attn(cache.cfg, cache.c, q, workspace=ws, max_tokens=most, max_q=m, scale=1.0)
+            nx.nx_read_device_status(cache.cfg, ws)
+            err = np.abs(_np(out) - o)
+            assert (err <= bound).all(), (m, most, float((err / bound).max()),
+                                          [float((err / (mag + 1e-30)).max(axis=(0, 2))[i]) for i in range(4)])
