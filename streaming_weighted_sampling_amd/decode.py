@@ -20,6 +20,12 @@ from .paged import (new_paged_cache, new_paged_workspace, nx_paged_append, nx_pa
                     nx_qk_norm_rope)
 
 
+def _not_captured(what):
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError(f"DecodeCache.{what} cannot be captured into a graph: the row bound, the query ring's place "
+                           "and the event number are the host's, a replay would not move them")
+
+
 class DecodeCache:
     """`n_seqs` sequences of one layer, up to `capacity` rows per head.
 
@@ -29,7 +35,8 @@ class DecodeCache:
     rewritten in place between events.
     Keys are rotated (and normed) once, when they arrive; evicted positions
     leave holes that nothing refers to again, so a kept row is stored as it was.
-    Evicting re-quantises the kept rows in their new blocks.  With cfg.block > 1 an
+    load, step and evict run eagerly (RuntimeError in a graph's capture; the nx_* calls they make can
+    be captured).  Evicting re-quantises the kept rows in their new blocks.  With cfg.block > 1 an
     event needs a row count that is a multiple of the block.
     """
 
@@ -86,6 +93,7 @@ class DecodeCache:
             raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)}: rows of {self.n_seqs} sequences expected")
         if rows > self.capacity:
             raise ValueError(f"{rows} rows, capacity {self.capacity}")
+        _not_captured("load")
         self.cache.lens.zero_()
         if rows:
             flat = [x.permute(0, 2, 1, 3).reshape(n * rows, hk, d) for x in (k, v)]
@@ -100,6 +108,7 @@ class DecodeCache:
             raise ValueError("the cache is full: evict first")
         if (self.rope is None) != (positions is None):
             raise ValueError("positions go with rope")
+        _not_captured("step")
         cfg = self.cfg
         q_rot = self.ring[:, :, self.queries % cfg.window]
         normed = self.k_weight is not None
@@ -126,6 +135,7 @@ class DecodeCache:
         kept = min(cfg.kept_rows(self.rows, self.head_cap), self.cap_rows)
         if kept == self.capacity and cfg.head_alloc == NX_HEADS_UNIFORM:
             raise ValueError(f"an event makes no room: its budget holds all {self.capacity} rows of the capacity")
+        _not_captured("evict")
         first = self.queries % w                 # the oldest query's place in the ring
         self.window[:, :, :w - first].copy_(self.ring[:, :, first:])
         self.window[:, :, w - first:].copy_(self.ring[:, :, :first])

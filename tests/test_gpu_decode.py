@@ -242,3 +242,24 @@ def test_an_event_that_makes_no_room_is_refused():
         dec.evict()
     dec.check()
     assert dec.step_no == 1 and all(torch.equal(a, b) for a, b in zip(_held(dec, 0, 1)[1:], before[1:]))
+
+
+def test_capture_of_the_driver_is_refused():
+    """Its host counters would not move with the replays: the ring's place and the row bound go wrong."""
+    dec = nx.DecodeCache(nx.NexusConfig(4, 2, 64, 4), 1, 64, 32, 2, page_blocks=1, device=DEV)
+    _fill(dec, 40, 5)
+    before = _held(dec, 0, 0)
+    args = _randn(3, 1, 8, 64, dtype="bf16").split((4, 2, 2), 1)
+    rows = torch.zeros(1, 2, 8, 64, dtype=torch.bfloat16, device=DEV)
+    for call in (lambda: dec.step(*args), dec.evict, lambda: dec.load(rows, rows)):
+        with pytest.raises(RuntimeError, match="captured"):
+            with torch.cuda.graph(torch.cuda.CUDAGraph()):
+                args[0] + 1                    # a graph of something
+                call()
+    torch.cuda.synchronize()
+    assert (dec.rows, dec.queries, dec.step_no) == (45, 5, 0)
+    assert all(torch.equal(a, b) for a, b in zip(_held(dec, 0, 0)[1:], before[1:]))
+    dec.step(*args)
+    dec.evict()
+    dec.check()
+    assert dec.rows == 32
