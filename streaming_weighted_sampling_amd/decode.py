@@ -12,6 +12,8 @@ is the capacity too: the next steps then need the counts).  Marshalling only; ev
 moves inside libnexus.so.
 """
 
+import functools
+
 import torch
 
 from ._lib import NX_CACHE_BLOCK, NX_HEADS_ALLOC, NX_HEADS_GIVEN, NX_HEADS_UNIFORM, NexusError
@@ -24,6 +26,15 @@ def _not_captured(what):
     if torch.cuda.is_current_stream_capturing():
         raise RuntimeError(f"DecodeCache.{what} cannot be captured into a graph: the row bound, the query ring's place "
                            "and the event number are the host's, a replay would not move them")
+
+
+def _on_own_device(method):
+    """The eviction calls work on the current GPU's current stream: make the cache's GPU the current one."""
+    @functools.wraps(method)
+    def call(self):
+        with torch.cuda.device(self.device):
+            return method(self)
+    return call
 
 
 class DecodeCache:
@@ -123,6 +134,7 @@ class DecodeCache:
         self.rows += 1
         return nx_paged_attn(cfg, self.cache, q_rot, workspace=self.ws, max_tokens=self.rows, out=self.out)
 
+    @_on_own_device
     def evict(self):
         """One eviction event over all sequences, back to the budget.  A head that the device rejects
         (check() raises) keeps all its rows.  A budget of the whole capacity is refused once the cache is
@@ -169,6 +181,7 @@ class DecodeCache:
         self.rows = kept if kept < self.capacity else max(0, int(self.cache.lens.max()))
         self.step_no += 1
 
+    @_on_own_device
     def check(self):
         """Synchronises and raises NexusError on an error that a step or an event recorded (both are
         cleared).  The cache can be used on: what was rejected is as it was before."""

@@ -314,3 +314,31 @@ def test_given_head_budgets_are_asked_for_and_checked(lib):
     with pytest.raises(ValueError, match="from 3 "):
         dec(n_sink=3, head_budget=[2, 9])
     assert dec(head_budget=[9, 60], head_cap=64).head_budget.tolist() == [[9, 60]] * 3
+
+
+def test_events_run_on_the_caches_own_gpu(lib, monkeypatch):
+    """Whatever GPU is current: the eviction calls take the current one's stream."""
+    from streaming_weighted_sampling_amd import decode
+    inside, ran = [None], []
+
+    class On:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            inside.append(self.device)
+
+        def __exit__(self, *a):
+            inside.pop()
+
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    for name in ("nx_paged_append", "nx_paged_gather", "nx_evict_batch", "nx_read_device_status"):
+        monkeypatch.setattr(decode, name, lambda *a, name=name, **kw: ran.append((name, inside[-1])))
+    dec = nx.DecodeCache(nx.NexusConfig(4, 2, 64, 4), 2, 64, 32, 2, device="cpu")
+    dec.rows = dec.queries = 40
+    dec.evict()
+    dec.check()
+    own = torch.device("cpu")
+    assert ("nx_evict_batch", own) in ran and ran.count(("nx_read_device_status", own)) == 2
+    assert all(device == own for _, device in ran)
