@@ -269,8 +269,16 @@ def nx_evict_batch(cfg, units_dev, n_units, max_tokens, walk_iters, seed, *, wor
 
 
 def nx_read_device_status(cfg, workspace, stream=None):
-    """Synchronises the stream and raises NexusError on a recorded device error
-    (workspace None: the status of nx_evict_step_noalloc calls on this device)."""
+    """Synchronises the stream (default: the current one of the workspace's GPU) and raises
+    NexusError on a recorded device error (workspace None: the status of
+    nx_evict_step_noalloc calls on the current device)."""
+    if workspace is not None and workspace.is_cuda and workspace.get_device() != torch.cuda.current_device():
+        with torch.cuda.device(workspace.get_device()):
+            return _read_device_status(cfg, workspace, stream)
+    return _read_device_status(cfg, workspace, stream)
+
+
+def _read_device_status(cfg, workspace, stream):
     d = cfg.desc(workspace, stream=stream)
     check(load().nx_read_device_status(ctypes.byref(d)), "device status")
 

@@ -342,3 +342,40 @@ def test_events_run_on_the_caches_own_gpu(lib, monkeypatch):
     own = torch.device("cpu")
     assert ("nx_evict_batch", own) in ran and ran.count(("nx_read_device_status", own)) == 2
     assert all(device == own for _, device in ran)
+
+
+def test_the_status_is_read_on_the_workspaces_gpu(monkeypatch):
+    """The paged calls run on the GPU of their tensors; the status read waits for that GPU's stream."""
+    from streaming_weighted_sampling_amd import api
+    current, seen = [0], []
+
+    class On:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            current.append(self.device)
+
+        def __exit__(self, *a):
+            current.pop()
+
+    class Workspace:
+        is_cuda = True
+
+        def __init__(self, device):
+            self.get_device = lambda: device
+            self.data_ptr, self.numel, self.element_size = (lambda: 4096), (lambda: 256), (lambda: 1)
+
+    class Library:
+        def nx_read_device_status(self, d):
+            seen.append(current[-1])
+            return 0
+
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[-1])
+    monkeypatch.setattr(api, "_stream_handle", lambda s: current[-1])
+    monkeypatch.setattr(api, "load", Library)
+    cfg = nx.NexusConfig(4, 2, 64, 4)
+    for device in (0, 3):
+        nx.nx_read_device_status(cfg, Workspace(device))
+    assert seen == [0, 3] and current == [0]
