@@ -100,14 +100,20 @@ class DecodeCache:
         """Replaces the rows: k, v [n_seqs, n_kv_heads, rows, D], keys already rotated (a prompt's
         rows, or the out_k / out_v of a first event)."""
         n, hk, rows, d = k.shape
-        if n != self.n_seqs or v.shape != k.shape:
-            raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)}: rows of {self.n_seqs} sequences expected")
+        if n != self.n_seqs or v.shape != k.shape or (hk, d) != (self.cfg.n_kv_heads, self.cfg.head_dim):
+            raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)}: rows of {self.n_seqs} sequences with "
+                             f"{self.cfg.n_kv_heads} heads of {self.cfg.head_dim} expected")
+        for x, name in ((k, "k"), (v, "v")):
+            if x.dtype != self.cfg.dtype:
+                raise TypeError(f"{name}: dtype {x.dtype}, expected {self.cfg.dtype}")
+            if x.device != self.device:
+                raise ValueError(f"{name} is on {x.device}, the cache on {self.device}")
         if rows > self.capacity:
             raise ValueError(f"{rows} rows, capacity {self.capacity}")
         _not_captured("load")
+        flat = [x.permute(0, 2, 1, 3).reshape(n * rows, hk, d) for x in (k, v)]
         self.cache.lens.zero_()
         if rows:
-            flat = [x.permute(0, 2, 1, 3).reshape(n * rows, hk, d) for x in (k, v)]
             nx_paged_append(self.cfg, self.cache, *flat, workspace=self.ws)
         self.rows, self.queries = rows, 0
 

@@ -263,3 +263,21 @@ def test_capture_of_the_driver_is_refused():
     dec.evict()
     dec.check()
     assert dec.rows == 32
+
+
+def _unchanged(dec, rows, queries, before):
+    S, hk = dec.n_seqs, dec.cfg.n_kv_heads
+    return (dec.rows, dec.queries) == (rows, queries) and dec.cache.lens.tolist() == [[rows] * hk] * S and \
+        all(torch.equal(a, b) for a, b in zip(_held(dec, 0, 0)[1:], before[1:]))
+
+
+def test_a_refused_load_leaves_the_rows():
+    dec = nx.DecodeCache(nx.NexusConfig(4, 2, 64, 4), 1, 128, 32, 1, page_blocks=1, device=DEV)
+    _fill(dec, 40, 9)
+    before = _held(dec, 0, 0)
+    rows = _randn(601, 1, 2, 20, 64, dtype="bf16")
+    for a, b in ((rows, rows.float()), (rows.float(), rows), (rows, rows.cpu()), (rows, rows[..., :32]),
+                 (rows[:, :1], rows[:, :1]), (rows[..., :32], rows[..., :32])):
+        with pytest.raises((ValueError, TypeError)):
+            dec.load(a, b)
+        assert _unchanged(dec, 49, 9, before)
