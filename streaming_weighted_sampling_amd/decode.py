@@ -69,8 +69,9 @@ class DecodeCache:
         self.cache.table.copy_(torch.arange(n_seqs * hk * pages, dtype=torch.int32).view(n_seqs, hk, pages))
         self.ws = new_paged_workspace(cfg, self.cache, capacity)
         self.out = torch.empty(n_seqs, cfg.n_q_heads, d, dtype=cfg.dtype, device=self.device)
-        # The last W rotated queries of every sequence, a ring over dimension 2.
-        self.ring = torch.zeros(n_seqs, cfg.n_q_heads, cfg.window, d, dtype=cfg.dtype, device=self.device)
+        # The last W rotated queries of every sequence, a ring over dimension 2; one place more, so that
+        # a step that is refused half-way has not overwritten the oldest of them.
+        self.ring = torch.zeros(n_seqs, cfg.n_q_heads, cfg.window + 1, d, dtype=cfg.dtype, device=self.device)
         self.queries = 0      # queries seen since load()
         self.rows = 0         # the host's bound on the heads' row counts
         self.step_no = 0      # eviction events
@@ -91,7 +92,7 @@ class DecodeCache:
                                  f"units) to {cap} expected")
             self.head_budget.copy_(given)
         self.counts = torch.zeros(n_seqs, hk, dtype=torch.int32, device=self.device)
-        self.window = torch.zeros_like(self.ring)
+        self.window = torch.zeros(n_seqs, cfg.n_q_heads, cfg.window, d, dtype=cfg.dtype, device=self.device)
         self.evict_ws = new_workspace(cfg, capacity, n_seqs, walk_iters, device=self.device)
         self.head_cap = cap
         self._units = {}
@@ -127,7 +128,7 @@ class DecodeCache:
             raise ValueError("positions go with rope")
         _not_captured("step")
         cfg = self.cfg
-        q_rot = self.ring[:, :, self.queries % cfg.window]
+        q_rot = self.ring[:, :, self.queries % (cfg.window + 1)]
         normed = self.k_weight is not None
         _, k_new = nx_qk_norm_rope(cfg, q, k if normed else None, workspace=self.ws, q_weight=self.q_weight,
                                    k_weight=self.k_weight, eps=self.eps, rope=self.rope, positions=positions,
@@ -154,9 +155,10 @@ class DecodeCache:
         if kept == self.capacity and cfg.head_alloc == NX_HEADS_UNIFORM:
             raise ValueError(f"an event makes no room: its budget holds all {self.capacity} rows of the capacity")
         _not_captured("evict")
-        first = self.queries % w                 # the oldest query's place in the ring
-        self.window[:, :, :w - first].copy_(self.ring[:, :, first:])
-        self.window[:, :, w - first:].copy_(self.ring[:, :, :first])
+        first = (self.queries + 1) % (w + 1)     # the oldest query's place in the ring
+        head = min(w, w + 1 - first)
+        self.window[:, :, :head].copy_(self.ring[:, :, first:first + head])
+        self.window[:, :, head:].copy_(self.ring[:, :, :w - head])
         nx_paged_gather(cfg, self.cache, workspace=self.ws, max_tokens=self.rows, out_k=self.k, out_v=self.v)
         units = self._units.get(self.rows)
         if units is None:

@@ -281,3 +281,20 @@ def test_a_refused_load_leaves_the_rows():
         with pytest.raises((ValueError, TypeError)):
             dec.load(a, b)
         assert _unchanged(dec, 49, 9, before)
+
+
+@pytest.mark.parametrize("window", [1, 4, 5])
+def test_a_refused_step_leaves_the_query_window(window):
+    dec = nx.DecodeCache(nx.NexusConfig(4, 2, 64, window), 1, 128, 32, 1, page_blocks=1, device=DEV)
+    _fill(dec, 40, 9)
+    qs = [_randn(202 + i, 1, 8, 64, dtype="bf16")[:, :4] for i in range(9)]
+    q, k, v = _randn(600, 1, 8, 64, dtype="bf16").split((4, 2, 2), 1)
+    before = _held(dec, 0, 0)
+    wide = torch.zeros(1, 2, 128, dtype=torch.bfloat16, device=DEV)
+    for bad in (v[:, :1], v.float(), wide[..., ::2], wide[..., 4:68], v.cpu()):
+        with pytest.raises((ValueError, TypeError, nx.NexusError)):
+            dec.step(q, k, bad)                # the query has taken its place by then
+        assert _unchanged(dec, 49, 9, before)
+    dec.evict()
+    dec.check()
+    assert torch.equal(dec.window, torch.stack(qs[-window:], 2))
