@@ -49,7 +49,8 @@ Range bytes_at(const void* p, int64_t n) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
   return {lo, lo + uintptr_t(n)};
 }
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
+// (An array of no bytes meets nothing, wherever it lies.)
+bool overlap(Range a, Range b) { return std::max(a.lo, b.lo) < std::min(a.hi, b.hi); }
 
 // A set of rows as the calls address it.
 struct RowSet {
@@ -374,7 +375,7 @@ nx_status nx_paged_gather(const nx_paged* cache, int32_t max_tokens, void* out_k
   }
   if (!aligned(out_k) || !aligned(out_v) || out_seq_stride * esz % 16 || out_head_stride * esz % 16)
     return NX_EUNSUPPORTED;
-  const int64_t n = ((cache->n_seqs - 1) * out_seq_stride + (hk - 1) * out_head_stride + rows) * esz;
+  const int64_t n = rows > 0 ? ((cache->n_seqs - 1) * out_seq_stride + (hk - 1) * out_head_stride + rows) * esz : 0;
   const Range ok = bytes_at(out_k, n), ov = bytes_at(out_v, n);
   const CacheRanges cr = cache_ranges(cache);
   if (overlap(ok, ov)) return NX_EALIAS;

@@ -379,3 +379,17 @@ def test_the_status_is_read_on_the_workspaces_gpu(monkeypatch):
     for device in (0, 3):
         nx.nx_read_device_status(cfg, Workspace(device))
     assert seen == [0, 3] and current == [0]
+
+
+def test_arrays_of_no_rows_meet_nothing(lib):
+    """Wherever an empty slice points: into the cache, the workspace, another array of the call."""
+    c = _cache(workspace_bytes=1 << 28)
+    for at in (4096, 7 * GB + 16, 8 * GB + 128, 20 * GB + 64):
+        assert lib.nx_paged_attn(c, _r(20, 4096), NxRows(FAKE + at, 4096, 128), 0, None, 100, 1, 0.0, None) == 0
+        assert lib.nx_paged_attn(c, _r(20, 4096), _r(21, 4096), 0, None, 100, 1, 0.0, FAKE + at) == 0
+        assert lib.nx_paged_gather(c, 0, FAKE + at, FAKE + at, 8 * 12800, 12800) == 0
+    d = NxDesc()
+    d.n_q_heads, d.n_kv_heads, d.head_dim, d.dtype = 32, 8, 128, _lib.NX_BF16
+    d.workspace, d.workspace_bytes = FAKE, 256
+    assert lib.nx_qk_norm_rope(d, None, 0, _r(20, 4096), NxRows(FAKE + 128, 4096, 128), None, None, None, None,
+                               1e-6) == 0
