@@ -371,7 +371,8 @@ enum { NX_ROPE_HALF = 0, NX_ROPE_PAIRS = 1 };  /* pairs (i, i + rot/2), or (2i, 
 #define NX_CACHE_BLOCK 32
 
 /* Rows of several heads: row r of head h starts at p + r * row_stride + h * head_stride
- * elements and holds head_dim contiguous elements of the call's dtype. */
+ * elements and holds head_dim contiguous elements of the call's dtype.  A stride between
+ * rows or heads of which the call has one only may be anything. */
 typedef struct nx_rows {
   void* p;
   int64_t row_stride;

@@ -56,8 +56,10 @@ bool overlap(Range a, Range b) { return std::max(a.lo, b.lo) < std::min(a.hi, b.
 struct RowSet {
   const nx_rows* r;
   int64_t n, heads, d, esz;
-  int64_t extent() const { return (heads - 1) * r->head_stride + d; }   // elements of one row's heads
-  Range range() const { return bytes_at(r->p, n ? ((n - 1) * r->row_stride + extent()) * esz : 0); }
+  int64_t extent() const { return (heads > 1 ? (heads - 1) * r->head_stride : 0) + d; }   // of one row's heads
+  Range range() const {
+    return bytes_at(r->p, n ? ((n > 1 ? (n - 1) * r->row_stride : 0) + extent()) * esz : 0);
+  }
 };
 
 // Exact for two sets that share a row stride which holds a whole row of each
@@ -65,22 +67,24 @@ struct RowSet {
 bool overlap(const RowSet& a, const RowSet& b) {
   if (!overlap(a.range(), b.range())) return false;
   const int64_t rs = a.r->row_stride;
-  if (rs == b.r->row_stride && a.extent() <= rs && b.extent() <= rs) {
+  if (a.n > 1 && rs == b.r->row_stride && a.extent() <= rs && b.extent() <= rs) {
     const int64_t diff = int64_t(reinterpret_cast<uintptr_t>(b.r->p) - reinterpret_cast<uintptr_t>(a.r->p));
     const int64_t at = ((diff / a.esz) % rs + rs) % rs;
     return !(at >= a.extent() && at + b.extent() <= rs);
   }
   return true;
 }
-bool same_rows(const nx_rows* a, const nx_rows* b) {
-  return a->p == b->p && a->row_stride == b->row_stride && a->head_stride == b->head_stride;
+// Strides between rows or heads of which there is one only may be anything.
+bool same_rows(const RowSet& a, const RowSet& b) {
+  return a.r->p == b.r->p && (a.n <= 1 || a.r->row_stride == b.r->row_stride) &&
+         (a.heads == 1 || a.r->head_stride == b.r->head_stride);
 }
 
 nx_status check_rows(const RowSet& s, bool output) {
   if (s.r == nullptr || (s.r->p == nullptr && s.n > 0)) return NX_EINVAL;
-  if (s.r->row_stride < 0 || s.r->head_stride < 0) return NX_EINVAL;
-  if (!aligned(s.r->p) || s.r->row_stride * s.esz % 16 || s.r->head_stride * s.esz % 16)
-    return NX_EUNSUPPORTED;
+  const int64_t row = s.n > 1 ? s.r->row_stride : 0, head = s.heads > 1 ? s.r->head_stride : 0;
+  if (row < 0 || head < 0) return NX_EINVAL;
+  if (!aligned(s.r->p) || row * s.esz % 16 || head * s.esz % 16) return NX_EUNSUPPORTED;
   if (output) {   // rows of an output must not share memory
     const bool by_row = (s.heads == 1 || s.r->head_stride >= s.d) && (s.n <= 1 || s.r->row_stride >= s.extent());
     const bool by_head = (s.n <= 1 || s.r->row_stride >= s.d) &&
@@ -223,10 +227,10 @@ nx_status nx_qk_norm_rope(const nx_desc* desc, const nx_rope* rope, int32_t n_ro
   const RowSet sq{q, n_rows, desc->n_q_heads, d, esz}, soq{out_q, n_rows, desc->n_q_heads, d, esz};
   const RowSet sk{k, n_rows, desc->n_kv_heads, d, esz}, sok{out_k, n_rows, desc->n_kv_heads, d, esz};
   if ((st = check_rows(sq, false)) != NX_OK || (st = check_rows(soq, true)) != NX_OK) return st;
-  if (!same_rows(q, out_q) && overlap(sq, soq)) return NX_EALIAS;
+  if (!same_rows(sq, soq) && overlap(sq, soq)) return NX_EALIAS;
   if (k != nullptr) {
     if ((st = check_rows(sk, false)) != NX_OK || (st = check_rows(sok, true)) != NX_OK) return st;
-    if (!same_rows(k, out_k) && overlap(sk, sok)) return NX_EALIAS;
+    if (!same_rows(sk, sok) && overlap(sk, sok)) return NX_EALIAS;
     if (overlap(soq, sk) || overlap(soq, sok) || overlap(sok, sq)) return NX_EALIAS;
   }
   for (const RowSet* o : {&soq, &sok}) {
@@ -278,7 +282,7 @@ nx_status nx_paged_append(const nx_paged* cache, const nx_rope* rope, const nx_r
   const RowSet sk{k, n_rows, cache->n_kv_heads, d, esz}, sv{v, n_rows, cache->n_kv_heads, d, esz};
   if ((st = check_rows(sk, false)) != NX_OK || (st = check_rows(sv, false)) != NX_OK) return st;
   // A block's 32 rows are addressed by 32-bit offsets.
-  if (std::max(k->row_stride, v->row_stride) * esz >= (int64_t(1) << 31) / kBlock - 4096) return NX_EUNSUPPORTED;
+  if (n_rows > 1 && std::max(k->row_stride, v->row_stride) * esz >= (int64_t(1) << 31) / kBlock - 4096) return NX_EUNSUPPORTED;
   const CacheRanges cr = cache_ranges(cache);
   const int64_t units = int64_t(cache->n_seqs) * cache->n_kv_heads;
   const Range lens = bytes_at(cache->lens, units * 4);

@@ -814,3 +814,20 @@ def test_attention_over_v_scales_far_apart(k, dtype, fmt, d, order):
             err = np.abs(_np(out) - o)
             assert (err <= bound).all(), (m, most, float((err / bound).max()),
                                           [float((err / (mag + 1e-30)).max(axis=(0, 2))[i]) for i in range(4)])
+
+
+def test_one_row_with_any_row_stride():
+    c = [Cache(1, 2, 2, 64, "bf16", "e4m3", 1, 4) for _ in range(2)]
+    x = _randn(7, 4, 64, dtype="bf16")
+    got = []
+    for row, other in zip((256, 1 << 40), c):
+        other.fill([31, 40])
+        k, q = (torch.as_strided(x, (1, n, 64), (row, 64, 1)) for n in (2, 4))
+        nx.nx_paged_append(other.cfg, other.c, k, k, workspace=other.ws)
+        n = nx.nx_qk_norm_rope(other.cfg, q, k, workspace=other.ws, q_weight=x[0], k_weight=x[1])
+        o = torch.as_strided(torch.empty(256, dtype=torch.bfloat16, device=DEV), (1, 4, 64), (row, 64, 1))
+        got.append((*n, nx.nx_paged_attn(other.cfg, other.c, q, workspace=other.ws, max_tokens=41, out=o),
+                    *nx.nx_paged_gather(other.cfg, other.c, workspace=other.ws, max_tokens=41)))
+        other.check()
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and other.c.lens.tolist() == [[32, 41]]
+    _check_attn(other, q, [1], got[1][2])

@@ -393,3 +393,20 @@ def test_arrays_of_no_rows_meet_nothing(lib):
     d.workspace, d.workspace_bytes = FAKE, 256
     assert lib.nx_qk_norm_rope(d, None, 0, _r(20, 4096), NxRows(FAKE + 128, 4096, 128), None, None, None, None,
                                1e-6) == 0
+
+
+def test_strides_of_a_single_row_or_head_do_not_matter(lib):
+    one = _ws(n_seqs=1, n_q_heads=1, n_kv_heads=1)
+    c = _ws()
+    start = FAKE + 40 * GB
+    for row in (3, 0, -8, 1 << 40):
+        q, o = NxRows(FAKE + 20 * GB, row, 128), NxRows(FAKE + 21 * GB, row, 128)
+        assert lib.nx_paged_attn(c, q, o, 1, start, 100, 1, 0.0, None) == EWORK       # as far as the workspace
+        assert lib.nx_paged_attn(c, q, q, 1, start, 100, 1, 0.0, None) == EALIAS
+        q, o = NxRows(FAKE + 20 * GB, 128, row), NxRows(FAKE + 21 * GB, 256, row)
+        assert lib.nx_paged_attn(one, q, o, 4, start, 100, 4, 0.0, None) == EWORK
+        d = NxDesc()
+        d.n_q_heads, d.n_kv_heads, d.head_dim, d.dtype = 4, 1, 128, _lib.NX_BF16
+        q, o = NxRows(FAKE + 20 * GB, row, 128), NxRows(FAKE + 20 * GB, 5, 128)
+        assert lib.nx_qk_norm_rope(d, None, 1, q, o, None, None, None, None, 1e-6) == EWORK     # in place
+        assert lib.nx_qk_norm_rope(d, None, 2, q, o, None, None, None, None, 1e-6) != EWORK
