@@ -233,15 +233,20 @@ nx_status nx_qk_norm_rope(const nx_desc* desc, const nx_rope* rope, int32_t n_ro
     if (!same_rows(sk, sok) && overlap(sk, sok)) return NX_EALIAS;
     if (overlap(soq, sk) || overlap(soq, sok) || overlap(sok, sq)) return NX_EALIAS;
   }
+  if (!aligned(q_weight) || !aligned(k_weight)) return NX_EUNSUPPORTED;
+  const Range status = bytes_at(desc->workspace, 256);
+  if (overlap(status, sq.range()) || (k != nullptr && overlap(status, sk.range())) || meets(status, rope, n_rows) ||
+      overlap(status, bytes_at(q_weight, q_weight != nullptr ? d * esz : 0)) ||
+      overlap(status, bytes_at(k_weight, k_weight != nullptr ? d * esz : 0)))
+    return NX_EALIAS;
   for (const RowSet* o : {&soq, &sok}) {
     if (o == &sok && k == nullptr) break;
     const Range r = o->range();
     if (meets(r, rope, n_rows) || overlap(r, bytes_at(q_weight, q_weight != nullptr ? d * esz : 0)) ||
         overlap(r, bytes_at(k_weight, k_weight != nullptr ? d * esz : 0)) ||
-        overlap(r, bytes_at(desc->workspace, 256)))
+        overlap(r, status))
       return NX_EALIAS;
   }
-  if (!aligned(q_weight) || !aligned(k_weight)) return NX_EUNSUPPORTED;
   if (desc->workspace == nullptr || desc->workspace_bytes < 256) return NX_EWORKSPACE;
   if (n_rows == 0) return NX_OK;
   if (int64_t(n_rows) * (int64_t(desc->n_q_heads) + desc->n_kv_heads) / (4096 / d) >= kMaxGrid - 1)
@@ -292,6 +297,10 @@ nx_status nx_paged_append(const nx_paged* cache, const nx_rope* rope, const nx_r
                        bytes_at(head_new, head_new != nullptr ? units * 4 : 0),
                        bytes_at(new_start, new_start != nullptr ? (int64_t(cache->n_seqs) + 1) * 4 : 0),
                        bytes_at(cache->workspace, 256)};
+  const Range& status = ins[5];
+  for (int i = 0; i < 5; ++i)
+    if (overlap(status, ins[i])) return NX_EALIAS;
+  if (meets(status, rope, n_rows)) return NX_EALIAS;
   for (int i = 0; i < 6; ++i) {
     for (int j = i + 1; j < 6; ++j)
       if (overlap(cr.r[i], cr.r[j])) return NX_EALIAS;
@@ -333,10 +342,16 @@ nx_status nx_paged_attn(const nx_paged* cache, const nx_rows* q, const nx_rows* 
   const CacheRanges cr = cache_ranges(cache);
   const Range lse = bytes_at(out_lse, out_lse != nullptr ? int64_t(n_rows) * cache->n_q_heads * 4 : 0);
   const int64_t units = int64_t(cache->n_seqs) * cache->n_kv_heads;
+  // (A workspace that is too small is refused below, not taken to reach into what follows it.)
   const Range ro = so.range(), ins[] = {
       bytes_at(cache->table, units * cache->max_pages * 4), bytes_at(cache->lens, units * 4),
       bytes_at(q_start, q_start != nullptr ? (int64_t(cache->n_seqs) + 1) * 4 : 0),
-      bytes_at(cache->workspace, int64_t(cut_bytes(cache, cut)))};
+      bytes_at(cache->workspace, int64_t(std::min(cache->workspace_bytes, cut_bytes(cache, cut))))};
+  for (int i = 0; i < 3; ++i)
+    if (overlap(ins[3], ins[i])) return NX_EALIAS;
+  if (overlap(ins[3], sq.range())) return NX_EALIAS;
+  for (const Range& x : cr.r)
+    if (overlap(ins[3], x)) return NX_EALIAS;
   for (const Range& x : cr.r)
     if (overlap(ro, x) || overlap(lse, x)) return NX_EALIAS;
   for (const Range& x : ins)
@@ -386,9 +401,12 @@ nx_status nx_paged_gather(const nx_paged* cache, int32_t max_tokens, void* out_k
   for (const Range& x : cr.r)
     if (overlap(ok, x) || overlap(ov, x)) return NX_EALIAS;
   const int64_t units = int64_t(cache->n_seqs) * hk;
-  for (const Range& x : {bytes_at(cache->table, units * cache->max_pages * 4), bytes_at(cache->lens, units * 4),
-                         bytes_at(cache->workspace, 256)})
-    if (overlap(ok, x) || overlap(ov, x)) return NX_EALIAS;
+  const Range status = bytes_at(cache->workspace, 256);
+  for (const Range& x : {bytes_at(cache->table, units * cache->max_pages * 4), bytes_at(cache->lens, units * 4)})
+    if (overlap(ok, x) || overlap(ov, x) || overlap(status, x)) return NX_EALIAS;
+  for (const Range& x : cr.r)
+    if (overlap(status, x)) return NX_EALIAS;
+  if (overlap(ok, status) || overlap(ov, status)) return NX_EALIAS;
   if (max_tokens == 0) return NX_OK;
   PagedArgs a = base_args(cache);
   a.max_tokens = max_tokens;

@@ -410,3 +410,33 @@ def test_strides_of_a_single_row_or_head_do_not_matter(lib):
         q, o = NxRows(FAKE + 20 * GB, row, 128), NxRows(FAKE + 20 * GB, 5, 128)
         assert lib.nx_qk_norm_rope(d, None, 1, q, o, None, None, None, None, 1e-6) == EWORK     # in place
         assert lib.nx_qk_norm_rope(d, None, 2, q, o, None, None, None, None, 1e-6) != EWORK
+
+
+def test_the_workspace_must_not_lie_over_the_inputs(lib):
+    """The status word and the attention's partials are written into it."""
+    arrays = {name: FAKE + i * GB for i, name in enumerate(
+        ("k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail", "table", "lens"))}
+    n = lib.nx_paged_workspace_bytes(_cache(), 100, 1)
+    for name, at in arrays.items():
+        c = _ws(workspace=at)
+        assert lib.nx_paged_append(c, None, _r(20), _r(21), 4, None, None, 1, None) == EALIAS, name
+        assert lib.nx_paged_attn(c, _r(20, 4096), _r(21, 4096), 4, None, 100, 1, 0.0, None) == EALIAS, name
+        assert lib.nx_paged_gather(c, 100, FAKE + 30 * GB, FAKE + 31 * GB, 8 * 12800, 12800) == EALIAS, name
+        c = _cache(workspace=at - n + 16, workspace_bytes=n)          # the partials only
+        assert lib.nx_paged_attn(c, _r(20, 4096), _r(21, 4096), 4, None, 100, 1, 0.0, None) == EALIAS, name
+        # too small a workspace is that, whatever follows it
+        c = _cache(workspace=at - 512, workspace_bytes=512)
+        assert lib.nx_paged_attn(c, _r(20, 4096), _r(21, 4096), 4, None, 100, 1, 0.0, None) == EWORK, name
+    rope = NxRope(FAKE + 41 * GB, FAKE + 42 * GB, 10, 64, 0)
+    for slot in (20, 21, 40, 41, 42, 43):
+        c = _ws(workspace=FAKE + slot * GB)
+        assert lib.nx_paged_append(c, rope, _r(20), _r(21), 4, FAKE + 40 * GB, FAKE + 43 * GB, 1, None) == EALIAS
+    for slot in (20, 40):
+        c = _ws(workspace=FAKE + slot * GB)
+        assert lib.nx_paged_attn(c, _r(20, 4096), _r(21, 4096), 4, FAKE + 40 * GB, 100, 1, 0.0, None) == EALIAS
+    for slot in (20, 22, 24, 25, 41, 42):
+        d = NxDesc()
+        d.n_q_heads, d.n_kv_heads, d.head_dim, d.dtype = 32, 8, 128, _lib.NX_BF16
+        d.workspace, d.workspace_bytes = FAKE + slot * GB, 256
+        assert lib.nx_qk_norm_rope(d, rope, 4, _r(20, 4096), _r(21, 4096), FAKE + 24 * GB, _r(22), _r(23),
+                                   FAKE + 25 * GB, 1e-6) == EALIAS, slot
