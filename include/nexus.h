@@ -353,8 +353,9 @@ nx_status nx_read_device_status(const nx_desc* desc);
  * matrix instruction that sums over rows.)
  *
  * Conventions are those above, and: bases and strides of q, k, v, out and the
- * cache arrays are multiples of 16 bytes (NX_EUNSUPPORTED otherwise).  What only
- * the device can see sets the bad-item bit of the device status: a sequence
+ * cache's codes and tails, and the bases of the norm weights, the rotation table and
+ * the workspace, are multiples of 16 bytes, those of the 32-bit arrays of 4
+ * (NX_EUNSUPPORTED otherwise).  What only the device can see sets the bad-item bit of the device status: a sequence
  * whose row range or row count is out of range is skipped (nx_paged_attn: its
  * output rows are unspecified); of a block whose page number is out of range
  * nx_paged_append stores nothing (the count still advances), nx_paged_gather

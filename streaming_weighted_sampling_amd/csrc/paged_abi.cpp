@@ -41,6 +41,8 @@ constexpr int64_t kStreamBytes = int64_t(64) << 20;
 
 int32_t elem_size(int32_t dtype) { return dtype == NX_BF16 ? 2 : 4; }
 bool aligned(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+// Of the 32-bit arrays: tables, counts, starts, positions, scales.
+bool words(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
 
 struct Range {
   uintptr_t lo, hi;
@@ -98,7 +100,7 @@ nx_status check_rope(const nx_rope* r, int32_t head_dim) {
   if (r == nullptr) return NX_OK;
   if (r->cos_sin == nullptr || r->n_pos < 1 || r->rot_dim < 0 || r->rot_dim > head_dim) return NX_EINVAL;
   if (r->style != NX_ROPE_HALF && r->style != NX_ROPE_PAIRS) return NX_EINVAL;
-  if (r->rot_dim % 16 || !aligned(r->cos_sin)) return NX_EUNSUPPORTED;
+  if (r->rot_dim % 16 || !aligned(r->cos_sin) || !words(r->positions)) return NX_EUNSUPPORTED;
   return NX_OK;
 }
 
@@ -142,6 +144,8 @@ nx_status check_cache(const nx_paged* c) {
       !c->lens)
     return NX_EINVAL;
   if (!aligned(c->k_codes) || !aligned(c->v_codes) || !aligned(c->k_tail) || !aligned(c->v_tail))
+    return NX_EUNSUPPORTED;
+  if (!words(c->k_scale) || !words(c->v_scale) || !words(c->table) || !words(c->lens) || !aligned(c->workspace))
     return NX_EUNSUPPORTED;
   if (c->workspace == nullptr || c->workspace_bytes < 256) return NX_EWORKSPACE;
   return NX_OK;
@@ -233,7 +237,7 @@ nx_status nx_qk_norm_rope(const nx_desc* desc, const nx_rope* rope, int32_t n_ro
     if (!same_rows(sk, sok) && overlap(sk, sok)) return NX_EALIAS;
     if (overlap(soq, sk) || overlap(soq, sok) || overlap(sok, sq)) return NX_EALIAS;
   }
-  if (!aligned(q_weight) || !aligned(k_weight)) return NX_EUNSUPPORTED;
+  if (!aligned(q_weight) || !aligned(k_weight) || !aligned(desc->workspace)) return NX_EUNSUPPORTED;
   const Range status = bytes_at(desc->workspace, 256);
   if (overlap(status, sq.range()) || (k != nullptr && overlap(status, sk.range())) || meets(status, rope, n_rows) ||
       overlap(status, bytes_at(q_weight, q_weight != nullptr ? d * esz : 0)) ||
@@ -280,6 +284,7 @@ nx_status nx_paged_append(const nx_paged* cache, const nx_rope* rope, const nx_r
   nx_status st = check_cache(cache);
   if (st != NX_OK) return st;
   if (n_rows < 0 || max_new < 0 || max_new > kMaxCacheRows) return NX_EINVAL;
+  if (!words(new_start) || !words(head_new) || !words(lens_out)) return NX_EUNSUPPORTED;
   if ((int64_t(max_new) / kBlock + 8) * cache->n_kv_heads >= kMaxGrid) return NX_EUNSUPPORTED;
   if (new_start == nullptr && int64_t(cache->n_seqs) * max_new > n_rows) return NX_EINVAL;
   if ((st = check_rope(rope, cache->head_dim)) != NX_OK) return st;
@@ -332,6 +337,7 @@ nx_status nx_paged_attn(const nx_paged* cache, const nx_rows* q, const nx_rows* 
   nx_status st = check_cache(cache);
   if (st != NX_OK) return st;
   if (n_rows < 0 || !std::isfinite(scale) || scale < 0.f) return NX_EINVAL;
+  if (!words(q_start) || !words(out_lse)) return NX_EUNSUPPORTED;
   if (q_start == nullptr && n_rows > 0 && int64_t(cache->n_seqs) * max_q > n_rows) return NX_EINVAL;
   Cut cut;
   if ((st = make_cut(cache, max_tokens, max_q, &cut)) != NX_OK) return st;

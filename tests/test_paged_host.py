@@ -440,3 +440,28 @@ def test_the_workspace_must_not_lie_over_the_inputs(lib):
         d.workspace, d.workspace_bytes = FAKE + slot * GB, 256
         assert lib.nx_qk_norm_rope(d, rope, 4, _r(20, 4096), _r(21, 4096), FAKE + 24 * GB, _r(22), _r(23),
                                    FAKE + 25 * GB, 1e-6) == EALIAS, slot
+
+
+def test_misaligned_arrays_are_refused(lib):
+    q, o, k, v = _r(20, 4096), _r(21, 4096), _r(22), _r(23)
+
+    def calls(c, start=None, head_new=None, lens_out=None, lse=None, rope=None):
+        return (lib.nx_paged_append(c, rope, k, v, 4, start, head_new, 1, lens_out),
+                lib.nx_paged_attn(c, q, o, 4, start, 100, 1, 0.0, lse))
+    for name in ("k_scale", "v_scale", "table", "lens"):
+        c = _ws()
+        setattr(c, name, getattr(c, name) + 2)
+        assert calls(c) == (EUNSUP, EUNSUP), name
+        assert lib.nx_paged_gather(c, 100, FAKE + 30 * GB, FAKE + 31 * GB, 8 * 12800, 12800) == EUNSUP
+    for off in (1, 4, 8):
+        c = _ws(workspace=FAKE + 8 * GB + off)
+        assert calls(c) == (EUNSUP, EUNSUP)
+        assert lib.nx_paged_gather(c, 100, FAKE + 30 * GB, FAKE + 31 * GB, 8 * 12800, 12800) == EUNSUP
+        d = NxDesc()
+        d.n_q_heads, d.n_kv_heads, d.head_dim, d.dtype = 32, 8, 128, _lib.NX_BF16
+        d.workspace, d.workspace_bytes = FAKE + off, 256
+        assert lib.nx_qk_norm_rope(d, None, 4, q, o, None, None, None, None, 1e-6) == EUNSUP
+    odd = FAKE + 40 * GB + 2
+    assert calls(_ws(), start=odd) == (EUNSUP, EUNSUP)
+    assert calls(_ws(), head_new=odd)[0] == calls(_ws(), lens_out=odd)[0] == calls(_ws(), lse=odd)[1] == EUNSUP
+    assert calls(_ws(), rope=NxRope(FAKE + 41 * GB, odd, 10, 64, 0))[0] == EUNSUP
