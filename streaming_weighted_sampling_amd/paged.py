@@ -20,6 +20,7 @@ from .api import _DTYPES, NexusConfig
 
 _FORMATS = {torch.float8_e4m3fn: NX_CACHE_E4M3, torch.int8: NX_CACHE_I8}
 _NAMES = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+_FIXED = frozenset(("cfg", "k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail", "table", "lens"))
 
 
 # The checks run on every call of a decode step, whose kernels take a few
@@ -121,7 +122,8 @@ class PagedCache:
     """The arrays of one paged 8-bit cache (layouts in include/nexus.h, nx_paged).
 
     The format is the dtype of the codes (float8_e4m3fn or int8).  table and
-    lens may be rewritten between calls (in place); the arrays themselves stay."""
+    lens may be rewritten between calls (in place); the arrays themselves stay
+    (assigning another raises AttributeError: make another PagedCache)."""
     cfg: NexusConfig
     k_codes: torch.Tensor      # [n_pages, page_blocks, 32, D]
     v_codes: torch.Tensor      # [n_pages, page_blocks, 4, D, 8]
@@ -158,6 +160,12 @@ class PagedCache:
         c.table = _tensor(self.table, "table", (n_seqs, hk, max_pages), torch.int32, dev)
         c.lens = _tensor(self.lens, "lens", (n_seqs, hk), torch.int32, dev)
         self._c = c
+
+    def __setattr__(self, name, value):
+        # The calls pass the addresses that _c took.
+        if name in _FIXED and self._c is not None and value is not getattr(self, name):
+            raise AttributeError(f"PagedCache.{name} cannot be replaced: write into it, or make another cache")
+        object.__setattr__(self, name, value)
 
     def _struct(self, cfg, workspace, stream):
         if cfg is not self.cfg and cfg != self.cfg:

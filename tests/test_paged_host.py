@@ -465,3 +465,19 @@ def test_misaligned_arrays_are_refused(lib):
     assert calls(_ws(), start=odd) == (EUNSUP, EUNSUP)
     assert calls(_ws(), head_new=odd)[0] == calls(_ws(), lens_out=odd)[0] == calls(_ws(), lse=odd)[1] == EUNSUP
     assert calls(_ws(), rope=NxRope(FAKE + 41 * GB, odd, 10, 64, 0))[0] == EUNSUP
+
+
+def test_a_caches_arrays_cannot_be_replaced():
+    """The calls would go on with the addresses of the old ones, whose memory may be gone."""
+    import dataclasses
+    cfg = nx.NexusConfig(4, 2, 64, 1, torch.bfloat16)
+    c = nx.new_paged_cache(cfg, 3, 8, 2, device="cpu")
+    for name in ("k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail", "table", "lens", "cfg"):
+        old = getattr(c, name)
+        with pytest.raises(AttributeError, match=name):
+            setattr(c, name, dataclasses.replace(old) if name == "cfg" else old.clone())
+        assert getattr(c, name) is old
+    c.lens.fill_(5)
+    c.table += 1
+    other = dataclasses.replace(c, lens=c.lens.clone())
+    assert other._c.lens == other.lens.data_ptr() != c.lens.data_ptr() == c._c.lens
