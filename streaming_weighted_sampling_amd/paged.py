@@ -10,7 +10,7 @@ made too; ordering that stream behind the inputs is the caller's).
 """
 
 import ctypes
-from dataclasses import dataclass, field
+from dataclasses import dataclass, field, replace
 
 import torch
 
@@ -159,6 +159,8 @@ class PagedCache:
         c.v_tail = _tensor(self.v_tail, "v_tail", (n_seqs, hk, 4, d, 8), cfg.dtype, dev)
         c.table = _tensor(self.table, "table", (n_seqs, hk, max_pages), torch.int32, dev)
         c.lens = _tensor(self.lens, "lens", (n_seqs, hk), torch.int32, dev)
+        # The shape that _c holds, whatever becomes of the caller's object.
+        self._cfg = replace(cfg)
         self._c = c
 
     def __setattr__(self, name, value):
@@ -267,9 +269,10 @@ def nx_paged_append(cfg, cache, k, v, *, workspace, max_new=None, new_start=None
     new_start: int32 [n_seqs + 1] first rows of the sequences (None: max_new rows each,
     default rows // n_seqs); head_new: int32 [n_seqs, n_kv_heads] rows each head takes of
     its sequence's; lens_out: int32 [n_seqs, n_kv_heads] (None: cache.lens is advanced)."""
-    dev, n, hk, s = cache._index, k.shape[0], cfg.n_kv_heads, cache.n_seqs
-    rk = _rows(cfg, k, "k", hk, dev, n)
-    rv = _rows(cfg, v, "v", hk, dev, n)
+    own, dev, n, s = cache._cfg, cache._index, k.shape[0], cache.n_seqs
+    hk = own.n_kv_heads
+    rk = _rows(own, k, "k", hk, dev, n)
+    rv = _rows(own, v, "v", hk, dev, n)
     max_new = _per_seq(cache, n, max_new, new_start, "max_new", "new_start")
     ns = _opt(new_start, "new_start", (s + 1,), torch.int32, dev)
     hn = _opt(head_new, "head_new", (s, hk), torch.int32, dev)
@@ -288,11 +291,12 @@ def nx_paged_attn(cfg, cache, q, *, workspace, max_tokens, max_q=None, q_start=N
     q_start: int32 [n_seqs + 1] first query rows of the sequences (None: max_q each, default
     rows // n_seqs); max_tokens: the expected longest head (any value is correct, and the
     workspace must have been made for at least it); out_lse: float32 [rows, n_q_heads]."""
-    dev, n, hq = cache._index, q.shape[0], cfg.n_q_heads
-    rq = _rows(cfg, q, "q", hq, dev, n)
+    own, dev, n = cache._cfg, cache._index, q.shape[0]
+    hq = own.n_q_heads
+    rq = _rows(own, q, "q", hq, dev, n)
     if out is None:
-        out = _new(lambda: torch.empty(n, hq, cfg.head_dim, dtype=cfg.dtype, device=q.device), stream)
-    ro = _rows(cfg, out, "out", hq, dev, n)
+        out = _new(lambda: torch.empty(n, hq, own.head_dim, dtype=own.dtype, device=q.device), stream)
+    ro = _rows(own, out, "out", hq, dev, n)
     max_q = _per_seq(cache, n, max_q, q_start, "max_q", "q_start") if n else 1      # no rows: nothing is done
     if scale is not None and not scale > 0:
         raise ValueError("scale must be positive")
@@ -307,16 +311,17 @@ def nx_paged_attn(cfg, cache, q, *, workspace, max_tokens, max_q=None, q_start=N
 def nx_paged_gather(cfg, cache, *, workspace, max_tokens, out_k=None, out_v=None, stream=None):
     """The cached rows as [n_seqs, n_kv_heads, >= max_tokens, D] tensors (rows past a head's
     length are left as they were; new outputs are zero-filled); returns (out_k, out_v)."""
-    shape, d = (cache.n_seqs, cfg.n_kv_heads, max_tokens, cfg.head_dim), cfg.head_dim
+    own, d = cache._cfg, cache._cfg.head_dim
+    shape = cache.n_seqs, own.n_kv_heads, max_tokens, d
     if out_k is None:
-        out_k = _new(lambda: torch.zeros(shape, dtype=cfg.dtype, device=cache.device), stream)
+        out_k = _new(lambda: torch.zeros(shape, dtype=own.dtype, device=cache.device), stream)
     if out_v is None:
         out_v = _new(lambda: torch.zeros_like(out_k), stream)
     for t, name in ((out_k, "out_k"), (out_v, "out_v")):
         got, st = t.shape, t.stride()
-        if t.dtype is not cfg.dtype or len(got) != 4 or got[:2] != shape[:2] or got[2] < max_tokens or \
+        if t.dtype is not own.dtype or len(got) != 4 or got[:2] != shape[:2] or got[2] < max_tokens or \
                 got[3] != d or t.get_device() != cache._index:
-            _bad(t, name, shape, cfg.dtype, cache._index)
+            _bad(t, name, shape, own.dtype, cache._index)
         if st[3] != 1 or st[2] != d:
             raise ValueError(f"{name}: rows must be contiguous")
     if out_k.stride() != out_v.stride():

@@ -481,3 +481,19 @@ def test_a_caches_arrays_cannot_be_replaced():
     c.table += 1
     other = dataclasses.replace(c, lens=c.lens.clone())
     assert other._c.lens == other.lens.data_ptr() != c.lens.data_ptr() == c._c.lens
+
+
+def test_a_changed_configuration_does_not_change_a_caches_shape():
+    """Rows are checked against the shape that the cache passes on, not against what its caller's
+    configuration has become."""
+    cfg = nx.NexusConfig(4, 2, 64, 1, torch.bfloat16)
+    c = nx.new_paged_cache(cfg, 3, 8, 2, device="cpu")
+    ws = torch.zeros(256, dtype=torch.uint8)
+    cfg.n_q_heads, cfg.n_kv_heads = 2, 1
+    q, k = torch.zeros(3, 2, 64).bfloat16(), torch.zeros(3, 1, 64).bfloat16()
+    with pytest.raises(ValueError, match="shape"):
+        nx.nx_paged_attn(cfg, c, q, workspace=ws, max_tokens=5)
+    with pytest.raises(ValueError, match="shape"):
+        nx.nx_paged_append(cfg, c, k, k, workspace=ws)
+    with pytest.raises(ValueError, match="shape"):
+        nx.nx_paged_gather(cfg, c, workspace=ws, max_tokens=5, out_k=torch.zeros(3, 1, 5, 64).bfloat16())
