@@ -169,9 +169,12 @@ class PagedCache:
             raise AttributeError(f"PagedCache.{name} cannot be replaced: write into it, or make another cache")
         object.__setattr__(self, name, value)
 
-    def _struct(self, cfg, workspace, stream):
+    def _same(self, cfg):
         if cfg is not self.cfg and cfg != self.cfg:
             raise ValueError("the cache was made for another configuration")
+
+    def _struct(self, cfg, workspace, stream):
+        self._same(cfg)
         if workspace.get_device() != self._index or not workspace.is_contiguous():
             raise ValueError(f"the workspace must be contiguous on {self.device}")
         # A copy: calls from several threads share the cache object.
@@ -203,6 +206,8 @@ def new_paged_cache(cfg, n_seqs, n_pages, max_pages, *, fmt="e4m3", page_blocks=
 
 
 def paged_workspace_bytes(cfg, cache, max_tokens, max_q=1):
+    """Bytes for calls on `cache` of up to max_tokens rows a head and max_q queries a sequence."""
+    cache._same(cfg)
     c = NxPaged.from_buffer_copy(cache._c)
     n = load().nx_paged_workspace_bytes(ctypes.byref(c), max_tokens, max_q)
     if n == 0:

@@ -497,3 +497,12 @@ def test_a_changed_configuration_does_not_change_a_caches_shape():
         nx.nx_paged_append(cfg, c, k, k, workspace=ws)
     with pytest.raises(ValueError, match="shape"):
         nx.nx_paged_gather(cfg, c, workspace=ws, max_tokens=5, out_k=torch.zeros(3, 1, 5, 64).bfloat16())
+
+
+def test_the_workspace_query_refuses_another_configuration(lib):
+    cfg = nx.NexusConfig(4, 2, 64, 1, torch.bfloat16)
+    c = nx.new_paged_cache(cfg, 3, 8, 2, device="cpu")
+    assert nx.paged_workspace_bytes(cfg, c, 100, 4) > 0
+    for make in (nx.paged_workspace_bytes, nx.new_paged_workspace):
+        with pytest.raises(ValueError, match="configuration"):
+            make(nx.NexusConfig(64, 2, 64, 1, torch.bfloat16), c, 100, 4)
