@@ -12,11 +12,12 @@ is the capacity too: the next steps then need the counts).  Marshalling only; ev
 moves inside libnexus.so.
 """
 
+import ctypes
 import functools
 
 import torch
 
-from ._lib import NX_CACHE_BLOCK, NX_HEADS_ALLOC, NX_HEADS_GIVEN, NX_HEADS_UNIFORM, NexusError
+from ._lib import NX_CACHE_BLOCK, NX_HEADS_ALLOC, NX_HEADS_GIVEN, NX_HEADS_UNIFORM, NexusError, NxUnit
 from .api import NexusConfig, make_units, new_workspace, nx_evict_batch, nx_read_device_status
 from .paged import (new_paged_cache, new_paged_workspace, nx_paged_append, nx_paged_attn, nx_paged_gather,
                     nx_qk_norm_rope)
@@ -95,7 +96,8 @@ class DecodeCache:
         self.window = torch.zeros(n_seqs, cfg.n_q_heads, cfg.window, d, dtype=cfg.dtype, device=self.device)
         self.evict_ws = new_workspace(cfg, capacity, n_seqs, walk_iters, device=self.device)
         self.head_cap = cap
-        self._units = {}
+        self._units = torch.zeros(n_seqs * ctypes.sizeof(NxUnit), dtype=torch.uint8, device=self.device)
+        self._units_rows = None
 
     def load(self, k, v):
         """Replaces the rows: k, v [n_seqs, n_kv_heads, rows, D], keys already rotated (a prompt's
@@ -160,23 +162,23 @@ class DecodeCache:
         self.window[:, :, :head].copy_(self.ring[:, :, first:first + head])
         self.window[:, :, head:].copy_(self.ring[:, :, :w - head])
         nx_paged_gather(cfg, self.cache, workspace=self.ws, max_tokens=self.rows, out_k=self.k, out_v=self.v)
-        units = self._units.get(self.rows)
-        if units is None:
+        if self._units_rows != self.rows:      # the event's records, in place: they differ in n_tokens only
             d, r = cfg.head_dim, self.cap_rows
-            units = self._units[self.rows] = make_units(
+            self._units.copy_(make_units(
                 [dict(q=self.window[s], k=self.k[s], v=self.v[s], keep=self.keep[s],
                       out_k=self.kept_k[0, s * r:], out_v=self.kept_v[0, s * r:],
                       kv_head_stride=self.capacity * d, out_head_stride=self.n_seqs * r * d,
                       n_tokens=self.rows, budget=self.budget, layer=self.layer, seq_id=s,
                       head_cap=self.head_cap, head_budget=self.head_budget[s],
                       head_tokens=self.cache.lens[s], head_tokens_out=self.counts[s])
-                 for s in range(self.n_seqs)], device=self.device)
+                 for s in range(self.n_seqs)], device="cpu"))
+            self._units_rows = self.rows
         # The event writes the count of every head that it serves; one that the device rejects keeps -1
         # here, and its rows as they were.
         self.counts.fill_(-1)
         if cfg.head_alloc == NX_HEADS_ALLOC:
             self.head_budget.fill_(-1)
-        nx_evict_batch(cfg, units, self.n_seqs, self.rows, self.walk_iters, self.seed, workspace=self.evict_ws,
+        nx_evict_batch(cfg, self._units, self.n_seqs, self.rows, self.walk_iters, self.seed, workspace=self.evict_ws,
                        step=self.step_no, max_out_rows=kept)
         if cfg.head_alloc == NX_HEADS_ALLOC and cfg.n_sink + cfg.n_recent == 0:
             # An allocation of no rows is not rejected (no row is forced): such a head keeps none.

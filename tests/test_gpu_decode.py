@@ -298,3 +298,24 @@ def test_a_refused_step_leaves_the_query_window(window):
     dec.evict()
     dec.check()
     assert torch.equal(dec.window, torch.stack(qs[-window:], 2))
+
+
+def test_events_at_many_row_counts_hold_no_more_memory():
+    """One set of event records, rewritten as the row count changes; each event as nx_evict_step has it."""
+    cfg = nx.NexusConfig(4, 2, 64, 4)
+    dec = nx.DecodeCache(cfg, 1, 128, 32, 1, page_blocks=1, seed=5, device=DEV)
+    ews = nx.new_workspace(cfg, 128, 1, 1, device=DEV)
+    held = None
+    for event, rows in enumerate((40, 41, 90, 40, 77, 78, 90, 41)):
+        _fill(dec, rows, 6, seed=700 + event)
+        n = dec.rows
+        k, v = nx.nx_paged_gather(cfg, dec.cache, workspace=dec.ws, max_tokens=n)
+        dec.evict()
+        dec.check()
+        want, _, _ = nx.nx_evict_step(cfg, dec.window[0], k[0], v[0], n, 32, 1, 5, workspace=ews, step=event)
+        assert torch.equal(want, dec.keep[0])
+        del k, v, want
+        torch.cuda.synchronize()
+        if event:
+            assert held is None or torch.cuda.memory_allocated() == held
+            held = torch.cuda.memory_allocated()
