@@ -47,7 +47,8 @@ class DecodeCache:
     rewritten in place between events.
     Keys are rotated (and normed) once, when they arrive; evicted positions
     leave holes that nothing refers to again, so a kept row is stored as it was.
-    load, step and evict run eagerly (RuntimeError in a graph's capture; the nx_* calls they make can
+    seed, layer and (with per-head budgets) budget may be changed between events; what sizes the buffers
+    is fixed.  load, step and evict run eagerly (RuntimeError in a graph's capture; the nx_* calls they make can
     be captured).  Evicting re-quantises the kept rows in their new blocks.  With cfg.block > 1 an
     event needs a row count that is a multiple of the block.
     """
@@ -97,7 +98,7 @@ class DecodeCache:
         self.evict_ws = new_workspace(cfg, capacity, n_seqs, walk_iters, device=self.device)
         self.head_cap = cap
         self._units = torch.zeros(n_seqs * ctypes.sizeof(NxUnit), dtype=torch.uint8, device=self.device)
-        self._units_rows = None
+        self._units_of = None
 
     def load(self, k, v):
         """Replaces the rows: k, v [n_seqs, n_kv_heads, rows, D], keys already rotated (a prompt's
@@ -153,8 +154,12 @@ class DecodeCache:
             raise ValueError(f"an event needs {w} queries, {self.queries} were seen")
         if self.rows % cfg.block:     # a short last block would be counted as a whole one
             raise ValueError(f"{self.rows} rows are not whole blocks of {cfg.block}")
+        uniform = cfg.head_alloc == NX_HEADS_UNIFORM
+        if (self.budget if uniform else self.head_cap) != self.keep.shape[2]:
+            raise ValueError(f"the event's buffers hold {self.keep.shape[2]} units a head: another "
+                             f"{'budget' if uniform else 'head_cap'} needs another DecodeCache")
         kept = min(cfg.kept_rows(self.rows, self.head_cap), self.cap_rows)
-        if kept == self.capacity and cfg.head_alloc == NX_HEADS_UNIFORM:
+        if kept == self.capacity and uniform:
             raise ValueError(f"an event makes no room: its budget holds all {self.capacity} rows of the capacity")
         _not_captured("evict")
         first = (self.queries + 1) % (w + 1)     # the oldest query's place in the ring
@@ -162,7 +167,8 @@ class DecodeCache:
         self.window[:, :, :head].copy_(self.ring[:, :, first:first + head])
         self.window[:, :, head:].copy_(self.ring[:, :, :w - head])
         nx_paged_gather(cfg, self.cache, workspace=self.ws, max_tokens=self.rows, out_k=self.k, out_v=self.v)
-        if self._units_rows != self.rows:      # the event's records, in place: they differ in n_tokens only
+        now = self.rows, self.budget, self.layer
+        if self._units_of != now:              # the event's records, rewritten in place
             d, r = cfg.head_dim, self.cap_rows
             self._units.copy_(make_units(
                 [dict(q=self.window[s], k=self.k[s], v=self.v[s], keep=self.keep[s],
@@ -172,7 +178,7 @@ class DecodeCache:
                       head_cap=self.head_cap, head_budget=self.head_budget[s],
                       head_tokens=self.cache.lens[s], head_tokens_out=self.counts[s])
                  for s in range(self.n_seqs)], device="cpu"))
-            self._units_rows = self.rows
+            self._units_of = now
         # The event writes the count of every head that it serves; one that the device rejects keeps -1
         # here, and its rows as they were.
         self.counts.fill_(-1)

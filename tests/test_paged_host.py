@@ -506,3 +506,39 @@ def test_the_workspace_query_refuses_another_configuration(lib):
     for make in (nx.paged_workspace_bytes, nx.new_paged_workspace):
         with pytest.raises(ValueError, match="configuration"):
             make(nx.NexusConfig(64, 2, 64, 1, torch.bfloat16), c, 100, 4)
+
+
+def test_an_event_reads_the_settings_of_its_time(lib, monkeypatch):
+    """Settings changed between events reach the event's records; those that the buffers were sized by
+    are refused."""
+    import contextlib
+
+    from streaming_weighted_sampling_amd import decode
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    seen = []
+    for name in ("nx_paged_append", "nx_paged_gather"):
+        monkeypatch.setattr(decode, name, lambda *a, **kw: None)
+    monkeypatch.setattr(decode, "nx_evict_batch", lambda cfg, units, n, rows, iters, seed, **kw: seen.append(
+        [(u.n_tokens, u.budget, u.layer, u.head_cap)
+         for u in (_lib.NxUnit * n).from_buffer_copy(bytes(units.numpy()))]))
+
+    def event(dec, rows):
+        dec.rows = dec.queries = rows
+        dec.evict()
+        return seen.pop()
+    dec = nx.DecodeCache(nx.NexusConfig(4, 2, 64, 4), 2, 64, 32, 2, layer=3, device="cpu")
+    assert event(dec, 40) == [(40, 32, 3, 32)] * 2 and event(dec, 41) == [(41, 32, 3, 32)] * 2
+    dec.layer = 5
+    assert event(dec, 40) == [(40, 32, 5, 32)] * 2
+    for budget in (33, 16):
+        dec.budget = budget
+        with pytest.raises(ValueError, match="budget"):
+            event(dec, 40)
+    per_head = nx.DecodeCache(nx.NexusConfig(4, 2, 64, 4, head_alloc=2), 2, 64, 20, 2, head_cap=30, device="cpu")
+    assert event(per_head, 40) == [(40, 20, 0, 30)] * 2
+    per_head.budget = 12
+    assert event(per_head, 40) == [(40, 12, 0, 30)] * 2
+    per_head.head_cap = 31
+    with pytest.raises(ValueError, match="head_cap"):
+        event(per_head, 40)
