@@ -22,4 +22,4 @@ from .paged import (  # noqa: F401
     PagedCache, Rope, rope_table, new_paged_cache, paged_workspace_bytes, new_paged_workspace,
     nx_qk_norm_rope, nx_paged_append, nx_paged_attn, nx_paged_gather,
 )
-from .decode import DecodeCache  # noqa: F401
+from .decode import DecodeCache, EventBuffers  # noqa: F401

@@ -14,6 +14,8 @@ moves inside libnexus.so.
 
 import ctypes
 import functools
+import weakref
+from dataclasses import replace
 
 import torch
 
@@ -38,6 +40,22 @@ def _on_own_device(method):
     return call
 
 
+class EventBuffers:
+    """What an event uses only while it runs: the rows read back from the cache, the kept ones as
+    [heads][seqs * cap_rows][D], and the event's workspace.  DecodeCaches of one configuration and size
+    (the layers of a model) can share one, as long as their events are ordered on one stream."""
+
+    def __init__(self, cfg, n_seqs, capacity, cap_rows, walk_iters, device):
+        hk, d = cfg.n_kv_heads, cfg.head_dim
+        self.shape = replace(cfg), n_seqs, capacity, cap_rows, walk_iters, device
+        self.k = torch.zeros(n_seqs, hk, capacity, d, dtype=cfg.dtype, device=device)
+        self.v = torch.zeros_like(self.k)
+        self.kept_k = torch.zeros(hk, n_seqs * cap_rows, d, dtype=cfg.dtype, device=device)
+        self.kept_v = torch.zeros_like(self.kept_k)
+        self.ws = new_workspace(cfg, capacity, n_seqs, walk_iters, device=device)
+        self.users = weakref.WeakSet()      # whose events report in this workspace
+
+
 class DecodeCache:
     """`n_seqs` sequences of one layer, up to `capacity` rows per head.
 
@@ -47,6 +65,8 @@ class DecodeCache:
     rewritten in place between events.
     Keys are rotated (and normed) once, when they arrive; evicted positions
     leave holes that nothing refers to again, so a kept row is stored as it was.
+    event_buffers: another DecodeCache's, to share them (by default each has its own, which are larger than
+    an unquantised cache would be).
     seed, layer and (with per-head budgets) budget may be changed between events; what sizes the buffers
     is fixed.  load, step and evict run eagerly (RuntimeError in a graph's capture; the nx_* calls they make can
     be captured).  Evicting re-quantises the kept rows in their new blocks.  With cfg.block > 1 an
@@ -55,7 +75,7 @@ class DecodeCache:
 
     def __init__(self, cfg: NexusConfig, n_seqs, capacity, budget, walk_iters, *, fmt="e4m3", page_blocks=4,
                  rope=None, q_weight=None, k_weight=None, eps=1e-6, seed=0, layer=0, head_cap=0, head_budget=None,
-                 device="cuda"):
+                 event_buffers=None, device="cuda"):
         if cfg.compact:
             raise ValueError("the kept rows are copied into new blocks: compact must be 0")
         if (cfg.head_alloc == NX_HEADS_GIVEN) != (head_budget is not None):
@@ -77,13 +97,16 @@ class DecodeCache:
         self.queries = 0      # queries seen since load()
         self.rows = 0         # the host's bound on the heads' row counts
         self.step_no = 0      # eviction events
-        # An event's buffers: all rows, and the kept ones as [heads][seqs * cap][D].
         cap = head_cap if head_cap and cfg.head_alloc != NX_HEADS_UNIFORM else budget
         self.cap_rows = min(cap * cfg.block, capacity)
-        self.k = torch.zeros(n_seqs, hk, capacity, d, dtype=cfg.dtype, device=self.device)
-        self.v = torch.zeros_like(self.k)
-        self.kept_k = torch.zeros(hk, n_seqs * self.cap_rows, d, dtype=cfg.dtype, device=self.device)
-        self.kept_v = torch.zeros_like(self.kept_k)
+        if event_buffers is None:
+            event_buffers = EventBuffers(cfg, n_seqs, capacity, self.cap_rows, walk_iters, self.device)
+        elif event_buffers.shape != (cfg, n_seqs, capacity, self.cap_rows, walk_iters, self.device):
+            raise ValueError("event_buffers were made for a cache of another configuration or size")
+        self._bufs = event_buffers
+        event_buffers.users.add(self)
+        self.k, self.v, self.evict_ws = event_buffers.k, event_buffers.v, event_buffers.ws
+        self.kept_k, self.kept_v = event_buffers.kept_k, event_buffers.kept_v
         self.keep = torch.zeros(n_seqs, hk, cap, dtype=torch.int32, device=self.device)
         self.head_budget = torch.zeros(n_seqs, hk, dtype=torch.int32, device=self.device)
         if head_budget is not None:
@@ -95,10 +118,13 @@ class DecodeCache:
             self.head_budget.copy_(given)
         self.counts = torch.zeros(n_seqs, hk, dtype=torch.int32, device=self.device)
         self.window = torch.zeros(n_seqs, cfg.n_q_heads, cfg.window, d, dtype=cfg.dtype, device=self.device)
-        self.evict_ws = new_workspace(cfg, capacity, n_seqs, walk_iters, device=self.device)
         self.head_cap = cap
         self._units = torch.zeros(n_seqs * ctypes.sizeof(NxUnit), dtype=torch.uint8, device=self.device)
         self._units_of = None
+
+    @property
+    def event_buffers(self):
+        return self._bufs
 
     def load(self, k, v):
         """Replaces the rows: k, v [n_seqs, n_kv_heads, rows, D], keys already rotated (a prompt's
@@ -149,7 +175,7 @@ class DecodeCache:
         """One eviction event over all sequences, back to the budget.  A head that the device rejects
         (check() raises) keeps all its rows.  A budget of the whole capacity is refused once the cache is
         full: nothing could follow."""
-        cfg, w = self.cfg, self.cfg.window
+        cfg, w, bufs = self.cfg, self.cfg.window, self.event_buffers
         if self.queries < w:
             raise ValueError(f"an event needs {w} queries, {self.queries} were seen")
         if self.rows % cfg.block:     # a short last block would be counted as a whole one
@@ -166,13 +192,13 @@ class DecodeCache:
         head = min(w, w + 1 - first)
         self.window[:, :, :head].copy_(self.ring[:, :, first:first + head])
         self.window[:, :, head:].copy_(self.ring[:, :, :w - head])
-        nx_paged_gather(cfg, self.cache, workspace=self.ws, max_tokens=self.rows, out_k=self.k, out_v=self.v)
+        nx_paged_gather(cfg, self.cache, workspace=self.ws, max_tokens=self.rows, out_k=bufs.k, out_v=bufs.v)
         now = self.rows, self.budget, self.layer
         if self._units_of != now:              # the event's records, rewritten in place
             d, r = cfg.head_dim, self.cap_rows
             self._units.copy_(make_units(
-                [dict(q=self.window[s], k=self.k[s], v=self.v[s], keep=self.keep[s],
-                      out_k=self.kept_k[0, s * r:], out_v=self.kept_v[0, s * r:],
+                [dict(q=self.window[s], k=bufs.k[s], v=bufs.v[s], keep=self.keep[s],
+                      out_k=bufs.kept_k[0, s * r:], out_v=bufs.kept_v[0, s * r:],
                       kv_head_stride=self.capacity * d, out_head_stride=self.n_seqs * r * d,
                       n_tokens=self.rows, budget=self.budget, layer=self.layer, seq_id=s,
                       head_cap=self.head_cap, head_budget=self.head_budget[s],
@@ -184,14 +210,14 @@ class DecodeCache:
         self.counts.fill_(-1)
         if cfg.head_alloc == NX_HEADS_ALLOC:
             self.head_budget.fill_(-1)
-        nx_evict_batch(cfg, self._units, self.n_seqs, self.rows, self.walk_iters, self.seed, workspace=self.evict_ws,
+        nx_evict_batch(cfg, self._units, self.n_seqs, self.rows, self.walk_iters, self.seed, workspace=bufs.ws,
                        step=self.step_no, max_out_rows=kept)
         if cfg.head_alloc == NX_HEADS_ALLOC and cfg.n_sink + cfg.n_recent == 0:
             # An allocation of no rows is not rejected (no row is forced): such a head keeps none.
             self.counts.masked_fill_((self.counts < 0) & (self.head_budget == 0) & (self.cache.lens <= self.rows), 0)
         self.cache.lens.masked_fill_(self.counts >= 0, 0)
         self.counts.clamp_(min=0)
-        nx_paged_append(cfg, self.cache, self.kept_k.permute(1, 0, 2), self.kept_v.permute(1, 0, 2),
+        nx_paged_append(cfg, self.cache, bufs.kept_k.permute(1, 0, 2), bufs.kept_v.permute(1, 0, 2),
                         workspace=self.ws, max_new=self.cap_rows, head_new=self.counts)
         # Where a head may keep as many rows as the cache holds, only the counts say how long the longest is.
         self.rows = kept if kept < self.capacity else max(0, int(self.cache.lens.max()))
@@ -200,13 +226,15 @@ class DecodeCache:
     @_on_own_device
     def check(self):
         """Synchronises and raises NexusError on an error that a step or an event recorded (both are
-        cleared).  The cache can be used on: what was rejected is as it was before."""
+        cleared; with shared event_buffers also an event of another cache).  The cache can be used on:
+        what was rejected is as it was before."""
         errors = []
-        for ws in (self.ws, self.evict_ws):
+        for ws in (self.ws, self.event_buffers.ws):
             try:
                 nx_read_device_status(self.cfg, ws)
             except NexusError as e:
                 errors.append(e)
         if errors:
-            self.rows = max(0, int(self.cache.lens.max()))     # a rejected head may be longer than the bound
+            for user in self.event_buffers.users:      # a rejected head may be longer than the bound
+                user.rows = max(0, int(user.cache.lens.max()))
             raise errors[0]

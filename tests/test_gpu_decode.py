@@ -319,3 +319,40 @@ def test_events_at_many_row_counts_hold_no_more_memory():
         if event:
             assert held is None or torch.cuda.memory_allocated() == held
             held = torch.cuda.memory_allocated()
+
+
+def test_layers_that_share_event_buffers():
+    """Each as with buffers of its own; an error is found by whichever is asked, for all of them."""
+    cfg = nx.NexusConfig(4, 2, 64, 4)
+
+    def layers(share):
+        made = []
+        for i in range(3):
+            made.append(nx.DecodeCache(cfg, 2, 128, 40, 2, page_blocks=1, seed=9, layer=i,
+                                       event_buffers=made[0].event_buffers if share and made else None, device=DEV))
+        return made
+    shared, own = layers(True), layers(False)
+    assert len({d.k.data_ptr() for d in shared}) == 1 and len({d.k.data_ptr() for d in own}) == 3
+    for event in range(2):
+        for both in (shared, own):
+            for i, dec in enumerate(both):
+                _fill(dec, 60 + 5 * i, 6, seed=800 + 40 * i + event)
+            for dec in both:
+                dec.evict()
+            for dec in both:
+                dec.check()
+        for a, b in zip(shared, own):
+            assert torch.equal(a.keep, b.keep) and a.rows == b.rows == 40
+            for s in range(2):
+                for h in range(2):
+                    x, y = _held(a, s, h), _held(b, s, h)
+                    assert x[0] == y[0] == 40 and all(torch.equal(p, q) for p, q in zip(x[1:], y[1:]))
+    for i, dec in enumerate(shared):
+        _fill(dec, 60 + 5 * i, 6, seed=900)
+    shared[1].rows -= 2                        # that layer's event rejects all heads
+    for dec in shared:
+        dec.evict()
+    with pytest.raises(nx.NexusError):
+        shared[2].check()
+    assert [d.rows for d in shared] == [40, 71, 40] and (shared[1].cache.lens == 71).all()
+    shared[0].check()                          # read once, then clear

@@ -542,3 +542,22 @@ def test_an_event_reads_the_settings_of_its_time(lib, monkeypatch):
     per_head.head_cap = 31
     with pytest.raises(ValueError, match="head_cap"):
         event(per_head, 40)
+
+
+def test_event_buffers_are_shared_by_caches_of_one_shape_only(lib):
+    cfg = nx.NexusConfig(4, 2, 64, 4)
+    first = nx.DecodeCache(cfg, 2, 64, 32, 2, device="cpu")
+    for kw in (dict(n_seqs=1), dict(capacity=96), dict(budget=30), dict(walk_iters=1),
+               dict(cfg=nx.NexusConfig(8, 2, 64, 4))):
+        with pytest.raises(ValueError, match="event_buffers"):
+            nx.DecodeCache(**(dict(cfg=cfg, n_seqs=2, capacity=64, budget=32, walk_iters=2) | kw),
+                           event_buffers=first.event_buffers, device="cpu")
+    second = nx.DecodeCache(cfg, 2, 64, 32, 2, layer=1, event_buffers=first.event_buffers, device="cpu")
+    alone = nx.DecodeCache(cfg, 2, 64, 32, 2, layer=1, device="cpu")
+    assert second.k is first.k and second.evict_ws is first.evict_ws and alone.k is not first.k
+    assert second.keep is not first.keep and second.cache is not first.cache
+    assert set(first.event_buffers.users) == {first, second}
+    with pytest.raises(AttributeError):
+        first.event_buffers = alone.event_buffers
+    del second
+    assert set(first.event_buffers.users) == {first}
