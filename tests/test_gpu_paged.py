@@ -831,3 +831,65 @@ def test_one_row_with_any_row_stride():
         other.check()
     assert all(torch.equal(a, b) for a, b in zip(*got)) and other.c.lens.tolist() == [[32, 41]]
     _check_attn(other, q, [1], got[1][2])
+
+
+@pytest.mark.parametrize("dtype,d,hkv,group,fmt", [("bf16", 128, 2, 4, "e4m3"), ("bf16", 64, 1, 8, "int8"),
+                                                   ("f32", 128, 1, 2, "int8"), ("f32", 64, 2, 5, "e4m3")])
+@pytest.mark.parametrize("m", [17, 65, 500])
+def test_attention_of_long_query_windows(m, dtype, d, hkv, group, fmt):
+    """Prompts and their last pieces, in 32-row tiles, whole heads and pieces: sequences that hold exactly the
+    queries' rows, more, and fewer (the oldest queries see nothing); causal borders inside blocks, tiles and
+    pieces."""
+    cache = Cache(3, hkv, group, d, dtype, fmt, 2, 24, max_q=m)
+    cache.fill([n - (7 * h if n > 7 else 0) for n in (m, 1500, max(1, m // 3)) for h in range(hkv)], seed=m)
+    counts = [m, m, m - 1]
+    q = _randn(110 + m, sum(counts), hkv * group, d, dtype=dtype)
+    start = torch.tensor([0, m, 2 * m, 3 * m - 1], dtype=torch.int32, device=DEV)
+    lse = torch.empty(len(q), hkv * group, device=DEV)
+    for most in (1000, 1500, 60000):           # whole heads, pieces of the listed lengths, many small ones
+        ws = nx.new_paged_workspace(cache.cfg, cache.c, most, m)
+        out = nx.nx_paged_attn(cache.cfg, cache.c, q, workspace=ws, max_tokens=most, max_q=m, q_start=start,
+                               out_lse=lse)
+        nx.nx_read_device_status(cache.cfg, ws)
+        _check_attn(cache, q, counts, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_of_a_whole_prompt(dtype):
+    """2048 queries over their own rows and 512 older ones."""
+    cache = Cache(1, 1, 1, 64, dtype, "int8", 8, 10, max_q=2048)
+    cache.fill([2560])
+    q = _randn(120, 2048, 1, 64, dtype=dtype)
+    out = nx.nx_paged_attn(cache.cfg, cache.c, q, workspace=cache.ws, max_tokens=2560)
+    cache.check()
+    _check_attn(cache, q, [2048], out)
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("f32", 128), ("bf16", 128)])
+def test_a_tiny_v_scale_under_the_largest_logit(dtype, d):
+    """One block holds nearly all of a row's weight and has a V scale far below (and zero, whose codes stand
+    for zeros), in the first, a middle and the last block, in one wavefront and across pieces."""
+    for at in (0, 20, 38):
+        for scale in (2.0 ** -50, 0.0):
+            cache = Cache(1, 1, 4, d, dtype, "int8", 1, 41, max_q=5)
+            cache.fill([39 * 32 + 5], seed=8)
+            page = int(cache.c.table[0, 0, at])
+            cache.c.k_scale[page] *= 8
+            cache.c.v_scale[page] = scale
+            q = _randn(130, 5, 4, d, dtype=dtype)
+            for m, most in ((1, 1253), (1, 50000), (5, 1000), (5, 50000)):
+                ws = nx.new_paged_workspace(cache.cfg, cache.c, most, m)
+                out = nx.nx_paged_attn(cache.cfg, cache.c, q[:m], workspace=ws, max_tokens=most, max_q=m)
+                nx.nx_read_device_status(cache.cfg, ws)
+                _check_attn(cache, q[:m], [m], out)
+
+
+def test_one_workspace_serves_windows_of_every_size():
+    """Made for the largest call; the calls of fewer queries cut their work otherwise."""
+    cache = Cache(1, 2, 8, 64, "bf16", "e4m3", 4, 12, max_q=64)
+    cache.fill([1500, 1333])
+    q = _randn(140, 64, 16, 64, dtype="bf16")
+    for m in (64, 57, 33, 16, 12, 9, 7, 2, 1, 64):
+        out = nx.nx_paged_attn(cache.cfg, cache.c, q[:m], workspace=cache.ws, max_tokens=1500)
+        cache.check()
+        _check_attn(cache, q[:m], [m], out)
