@@ -401,7 +401,7 @@ typedef struct nx_paged {
   int32_t format;            /* NX_CACHE_E4M3 or NX_CACHE_I8 */
   int32_t page_blocks;       /* blocks per page: a power of two, at most 1024 */
   int32_t n_pages;
-  int32_t max_pages;         /* table entries per (sequence, head) */
+  int32_t max_pages;         /* table entries per (sequence, head): at most 2^29 rows */
   void* k_codes;
   void* v_codes;
   float* k_scale;

@@ -11,6 +11,8 @@ using namespace nx;
 namespace {
 
 constexpr int64_t kMaxCacheRows = int64_t(1) << 24;
+// What a head's table may hold: the attention sums 64 heads' blocks in 32 bits.
+constexpr int64_t kMaxHeadRows = int64_t(1) << 29;
 constexpr int64_t kMaxGrid = int64_t(1) << 23;   // workgroups of up to 512 threads: 2^32 threads
 constexpr int64_t kCUs = 256;
 // Workgroups per CU that an attention call is cut into.  16-row tiles: one
@@ -122,6 +124,7 @@ nx_status check_shape(const nx_paged* c) {
   if (c->n_q_heads / c->n_kv_heads > 256) return NX_EUNSUPPORTED;
   if (int64_t(c->n_seqs) * c->n_kv_heads > 65535) return NX_EUNSUPPORTED;     // grid y
   if (int64_t(c->n_pages) * c->page_blocks > INT32_MAX) return NX_EUNSUPPORTED;
+  if (int64_t(c->max_pages) * c->page_blocks * kBlock > kMaxHeadRows) return NX_EUNSUPPORTED;
   return NX_OK;
 }
 

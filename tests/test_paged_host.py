@@ -561,3 +561,12 @@ def test_event_buffers_are_shared_by_caches_of_one_shape_only(lib):
         first.event_buffers = alone.event_buffers
     del second
     assert set(first.event_buffers.users) == {first}
+
+
+def test_tables_of_more_rows_than_are_counted_in_32_bits(lib):
+    """64 heads of 2^31 rows are 2^32 blocks, which the attention's cut would add up in 32 bits."""
+    for pages, blocks, code in ((1 << 14, 1024, EWORK), ((1 << 14) + 1, 1024, EUNSUP), (1 << 16, 1024, EUNSUP),
+                                (1 << 24, 1, EWORK), (1 << 30, 1, EUNSUP), ((1 << 31) - 1, 64, EUNSUP)):
+        c = _cache(max_pages=pages, page_blocks=blocks, n_seqs=1, n_kv_heads=1, n_q_heads=1)
+        assert lib.nx_paged_attn(c, _r(20, 4096), _r(21, 4096), 4, None, 100, 1, 0.0, None) == code, (pages, blocks)
+        assert (lib.nx_paged_workspace_bytes(c, 100, 1) > 0) == (code == EWORK)
