@@ -491,7 +491,8 @@ nx_status nx_paged_attn(const nx_paged* cache, const nx_rows* q, const nx_rows* 
  * (s, h) at out_k + s * out_seq_stride + h * out_head_stride + t * head_dim
  * elements, and likewise for V; other rows are left as they were.  max_tokens
  * bounds the counts (a longer head is marked bad and skipped);
- * out_head_stride >= max_tokens * head_dim.
+ * out_head_stride >= max_tokens * head_dim and out_seq_stride >= (n_kv_heads - 1) *
+ * out_head_stride + max_tokens * head_dim, where there is more than one head or sequence.
  */
 nx_status nx_paged_gather(const nx_paged* cache, int32_t max_tokens, void* out_k, void* out_v,
                           int64_t out_seq_stride, int64_t out_head_stride);

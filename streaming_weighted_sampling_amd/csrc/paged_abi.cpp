@@ -398,9 +398,9 @@ nx_status nx_paged_gather(const nx_paged* cache, int32_t max_tokens, void* out_k
   if (max_tokens < 0 || max_tokens > kMaxCacheRows || out_k == nullptr || out_v == nullptr) return NX_EINVAL;
   const int64_t d = cache->head_dim, esz = elem_size(cache->dtype), hk = cache->n_kv_heads;
   const int64_t rows = int64_t(max_tokens) * d;
-  if (out_head_stride < rows || out_seq_stride < (hk - 1) * out_head_stride + rows) {
-    if (!(cache->n_seqs == 1 && out_head_stride >= rows)) return NX_EINVAL;
-  }
+  if (hk == 1) out_head_stride = rows;   // (strides of one head or sequence may be anything)
+  if (cache->n_seqs == 1) out_seq_stride = (hk - 1) * out_head_stride + rows;
+  if (out_head_stride < rows || out_seq_stride < (hk - 1) * out_head_stride + rows) return NX_EINVAL;
   if (!aligned(out_k) || !aligned(out_v) || out_seq_stride * esz % 16 || out_head_stride * esz % 16)
     return NX_EUNSUPPORTED;
   const int64_t n = rows > 0 ? ((cache->n_seqs - 1) * out_seq_stride + (hk - 1) * out_head_stride + rows) * esz : 0;

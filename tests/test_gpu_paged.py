@@ -893,3 +893,16 @@ def test_one_workspace_serves_windows_of_every_size():
         out = nx.nx_paged_attn(cache.cfg, cache.c, q[:m], workspace=cache.ws, max_tokens=1500)
         cache.check()
         _check_attn(cache, q[:m], [m], out)
+
+
+def test_gather_into_views_of_one_head_or_sequence():
+    for s, h in ((1, 3), (3, 1), (1, 1)):
+        cache = Cache(s, h, 1, 64, "bf16", "e4m3", 1, 4)
+        cache.fill([40 + i for i in range(s * h)])
+        k, v = nx.nx_paged_gather(cache.cfg, cache.c, workspace=cache.ws, max_tokens=44)
+        a = [torch.zeros(s * h * 44 * 64, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        strides = (5 if s == 1 else 44 * 64, 7 if h == 1 else 44 * 64, 64, 1)
+        o = [torch.as_strided(x, (s, h, 44, 64), strides) for x in a]
+        nx.nx_paged_gather(cache.cfg, cache.c, workspace=cache.ws, max_tokens=44, out_k=o[0], out_v=o[1])
+        cache.check()
+        assert torch.equal(a[0], k.flatten()) and torch.equal(a[1], v.flatten())

@@ -570,3 +570,15 @@ def test_tables_of_more_rows_than_are_counted_in_32_bits(lib):
         c = _cache(max_pages=pages, page_blocks=blocks, n_seqs=1, n_kv_heads=1, n_q_heads=1)
         assert lib.nx_paged_attn(c, _r(20, 4096), _r(21, 4096), 4, None, 100, 1, 0.0, None) == code, (pages, blocks)
         assert (lib.nx_paged_workspace_bytes(c, 100, 1) > 0) == (code == EWORK)
+
+
+def test_gather_strides_of_a_single_head_or_sequence_do_not_matter(lib):
+    def call(seqs, heads, ss, hs):
+        c = _ws(n_seqs=seqs, n_kv_heads=heads, n_q_heads=heads, k_tail=FAKE + 30 * GB)     # under out_k
+        return lib.nx_paged_gather(c, 100, FAKE + 30 * GB, FAKE + 31 * GB, ss, hs)
+    for odd in (0, 3, -8, 1 << 40):
+        assert call(1, 8, odd, 12800) == EALIAS            # as far as the last check
+        assert call(4, 1, 12800, odd) == EALIAS
+        assert call(1, 1, odd, odd) == EALIAS
+    assert call(2, 1, 12799, 12800) == EINVAL and call(1, 2, 0, 12799) == EINVAL
+    assert call(2, 2, 25600 - 1, 12800) == EINVAL
