@@ -425,7 +425,9 @@ size_t nx_paged_workspace_bytes(const nx_paged* cache, int32_t max_tokens, int32
 /*
  * Root-mean-square norm of every query and key head, then the position rotation,
  * in one pass: y = x * weight / sqrt(mean(x^2) + eps), rounded once after the
- * rotation.  Statistics and rotation are fp32.
+ * rotation.  Statistics and rotation are fp32: a row's largest element must stay below
+ * 2^60 (past 2^63 the squares overflow and the row becomes 0) and, where eps is 0, above
+ * 2^-60.
  *   desc      n_q_heads, n_kv_heads, head_dim, dtype, stream, and a workspace of
  *             >= 256 bytes for the status word
  *   rope      nullable: no rotation
