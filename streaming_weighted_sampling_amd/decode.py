@@ -94,6 +94,7 @@ class DecodeCache:
         # The last W rotated queries of every sequence, a ring over dimension 2; one place more, so that
         # a step that is refused half-way has not overwritten the oldest of them.
         self.ring = torch.zeros(n_seqs, cfg.n_q_heads, cfg.window + 1, d, dtype=cfg.dtype, device=self.device)
+        self._places = [self.ring[:, :, i] for i in range(cfg.window + 1)]
         self.queries = 0      # queries seen since load()
         self.rows = 0         # the host's bound on the heads' row counts
         self.step_no = 0      # eviction events
@@ -157,7 +158,7 @@ class DecodeCache:
             raise ValueError("positions go with rope")
         _not_captured("step")
         cfg = self.cfg
-        q_rot = self.ring[:, :, self.queries % (cfg.window + 1)]
+        q_rot = self._places[self.queries % len(self._places)]
         normed = self.k_weight is not None
         _, k_new = nx_qk_norm_rope(cfg, q, k if normed else None, workspace=self.ws, q_weight=self.q_weight,
                                    k_weight=self.k_weight, eps=self.eps, rope=self.rope, positions=positions,
@@ -215,8 +216,7 @@ class DecodeCache:
         if cfg.head_alloc == NX_HEADS_ALLOC and cfg.n_sink + cfg.n_recent == 0:
             # An allocation of no rows is not rejected (no row is forced): such a head keeps none.
             self.counts.masked_fill_((self.counts < 0) & (self.head_budget == 0) & (self.cache.lens <= self.rows), 0)
-        self.cache.lens.masked_fill_(self.counts >= 0, 0)
-        self.counts.clamp_(min=0)
+        self.cache.lens.masked_fill_(self.counts >= 0, 0)      # (the append leaves a head whose count is -1)
         nx_paged_append(cfg, self.cache, bufs.kept_k.permute(1, 0, 2), bufs.kept_v.permute(1, 0, 2),
                         workspace=self.ws, max_new=self.cap_rows, head_new=self.counts)
         # Where a head may keep as many rows as the cache holds, only the counts say how long the longest is.

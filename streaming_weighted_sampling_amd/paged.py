@@ -170,11 +170,12 @@ class PagedCache:
         object.__setattr__(self, name, value)
 
     def _same(self, cfg):
-        if cfg is not self.cfg and cfg != self.cfg:
+        if cfg != self.cfg:
             raise ValueError("the cache was made for another configuration")
 
     def _struct(self, cfg, workspace, stream):
-        self._same(cfg)
+        if cfg is not self.cfg:
+            self._same(cfg)
         if workspace.get_device() != self._index or not workspace.is_contiguous():
             raise ValueError(f"the workspace must be contiguous on {self.device}")
         # A copy: calls from several threads share the cache object.
