@@ -90,10 +90,10 @@ class Rope:
     cos_sin: torch.Tensor
     pairs: bool = False
 
-    def __post_init__(self):
-        t = self.cos_sin
-        if t.dim() != 2 or t.dtype != torch.float32 or not t.is_contiguous():
+    def __setattr__(self, name, t):       # also where the table is replaced later
+        if name == "cos_sin" and (t.dim() != 2 or t.dtype != torch.float32 or not t.is_contiguous()):
             raise ValueError("cos_sin must be a contiguous float32 [n_pos, rot_dim] tensor")
+        object.__setattr__(self, name, t)
 
     def _struct(self, positions, n_rows, index):
         t = self.cos_sin

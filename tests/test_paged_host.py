@@ -582,3 +582,14 @@ def test_gather_strides_of_a_single_head_or_sequence_do_not_matter(lib):
         assert call(1, 1, odd, odd) == EALIAS
     assert call(2, 1, 12799, 12800) == EINVAL and call(1, 2, 0, 12799) == EINVAL
     assert call(2, 2, 25600 - 1, 12800) == EINVAL
+
+
+def test_a_replaced_rotation_table_is_checked():
+    """A table of another type or shape would be read as float32 rows, past its end."""
+    rope = nx.Rope(torch.zeros(4, 16))
+    for bad in (torch.zeros(4, 16, dtype=torch.float16), torch.zeros(64), torch.zeros(4, 32)[:, ::2]):
+        with pytest.raises(ValueError, match="cos_sin"):
+            rope.cos_sin = bad
+    rope.cos_sin = longer = torch.zeros(9, 16)
+    rope.pairs = True
+    assert rope.cos_sin is longer and rope.pairs
