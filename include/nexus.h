@@ -352,20 +352,20 @@ nx_status nx_read_device_status(const nx_desc* desc);
  * (V is stored 8 rows deep so that 8 consecutive bytes are one operand of the
  * matrix instruction that sums over rows.)
  *
- * Conventions are those above, and: bases and strides of q, k, v, out and the
- * cache's codes and tails, and the bases of the norm weights, the rotation table and
- * the workspace, are multiples of 16 bytes, those of the 32-bit arrays of 4
- * (NX_EUNSUPPORTED otherwise).  What only the device can see sets the bad-item bit of the device status: a sequence
- * whose row range or row count is out of range is skipped (nx_paged_attn: its
- * output rows are unspecified); of a block whose page number is out of range
- * nx_paged_append stores nothing (the count still advances), nx_paged_gather
- * writes nothing, and nx_paged_attn reads page 0 in its place.  A call's pages
- * are distinct for the (sequence, head)s that it writes; pages that are only
- * read may be shared.  Outputs that overlap another array of the call are
- * refused (NX_EALIAS), also the small ones and the workspace.  A call of no rows is
- * valid.  Calls that may run at the same time have workspaces of their own.
- * The per-stage profiler covers the eviction stages only.  With NX_DEBUG set these
- * calls are synchronous too.
+ * Conventions are those above, and: bases and strides of q, k, v, out and the cache's
+ * codes and tails, and the bases of the norm weights, the rotation table and the
+ * workspace, are multiples of 16 bytes, those of the 32-bit arrays of 4
+ * (NX_EUNSUPPORTED otherwise).  What only the device can see sets the bad-item bit of
+ * the device status: a sequence whose row range or row count is out of range is
+ * skipped (nx_paged_attn: its output rows are unspecified); of a block whose page
+ * number is out of range nx_paged_append stores nothing (the count still advances),
+ * nx_paged_gather writes nothing, and nx_paged_attn reads page 0 in its place.  A
+ * call's pages are distinct for the (sequence, head)s that it writes; pages that are
+ * only read may be shared.  Outputs that overlap another array of the call are refused
+ * (NX_EALIAS), also the small ones and the workspace.  A call of no rows is valid.
+ * Calls that may run at the same time have workspaces of their own. The per-stage
+ * profiler covers the eviction stages only.  With NX_DEBUG set these calls are
+ * synchronous too.
  */
 enum { NX_CACHE_E4M3 = 0, NX_CACHE_I8 = 1 };   /* 8-bit codes: OCP e4m3, signed integer */
 enum { NX_ROPE_HALF = 0, NX_ROPE_PAIRS = 1 };  /* pairs (i, i + rot/2), or (2i, 2i + 1) */
