@@ -356,3 +356,29 @@ def test_layers_that_share_event_buffers():
         shared[2].check()
     assert [d.rows for d in shared] == [40, 71, 40] and (shared[1].cache.lens == 71).all()
     shared[0].check()                          # read once, then clear
+
+
+def test_the_whole_loop_on_a_side_stream():
+    """Load, steps and events under another current stream, while the default stream is busy."""
+    cfg = nx.NexusConfig(4, 2, 64, 4)
+
+    def loop():
+        dec = nx.DecodeCache(cfg, 2, 96, 32, 2, page_blocks=1, seed=3, device=DEV)
+        _fill(dec, 60, 36)
+        outs = []
+        for event in range(2):
+            dec.evict()
+            for i in range(64):
+                outs.append(dec.step(*_randn(1000 + i + 64 * event, 2, 8, 64, dtype="bf16").split((4, 2, 2), 1)).clone())
+        dec.check()
+        return torch.stack(outs), dec.cache.lens.clone(), dec.keep.clone()
+    want = loop()
+    torch.cuda.synchronize()
+    big, side = torch.randn(4096, 4096, device=DEV), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        big @ big
+    with torch.cuda.stream(side):
+        got = loop()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
